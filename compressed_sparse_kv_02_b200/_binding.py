@@ -26,6 +26,7 @@ ERR_WORKSPACE = -3
 ERR_CUDA = -4
 ERR_TIMEOUT = -5
 ERR_OUT_OF_RANGE = -6
+ERR_NO_PAGES = -7
 
 BF16, F32, FP8_E4M3, FP4_E2M1 = 0, 1, 2, 3
 LAYER_CSA, LAYER_HCA = 0, 1
@@ -90,11 +91,45 @@ class AttendArgs(ctypes.Structure):
     ]
 
 
+class ForkArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("layer", ctypes.POINTER(LayerStruct)), ("page_refs", _P), ("n", _I32),
+        ("src_seqs", _P), ("dst_seqs", _P), ("n_entries", _P), ("d_status", _P),
+    ]
+
+
+class FreeArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("layer", ctypes.POINTER(LayerStruct)), ("page_refs", _P), ("n_seq", _I32),
+        ("seq_ids", _P), ("keep", _P), ("d_status", _P),
+    ]
+
+
+class ReserveArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("layer", ctypes.POINTER(LayerStruct)), ("page_refs", _P), ("n_seq", _I32),
+        ("seq_ids", _P), ("first", _P), ("count", _P), ("max_count", _I64), ("d_status", _P),
+    ]
+
+
+class CompactArgs(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_uint32), ("src", ctypes.POINTER(LayerStruct)), ("dst", ctypes.POINTER(LayerStruct)),
+        ("src_refs", _P), ("dst_refs", _P), ("d_status", _P),
+    ]
+
+
 SYMBOLS = {
     "cskv_layer_bytes": (_I32, [ctypes.POINTER(LayerStruct)] + [ctypes.POINTER(ctypes.c_size_t)] * 8),
     "csa_compress_kv": (_I32, [ctypes.POINTER(CompressArgs), _P]),
     "hca_compress_kv": (_I32, [ctypes.POINTER(CompressArgs), _P]),
     "cskv_cache_append": (_I32, [ctypes.POINTER(AppendArgs), _P]),
+    "cskv_cache_fork": (_I32, [ctypes.POINTER(ForkArgs), _P]),
+    "cskv_cache_free": (_I32, [ctypes.POINTER(FreeArgs), _P]),
+    "cskv_reserve_ws_bytes": (_I32, [ctypes.POINTER(ReserveArgs), ctypes.POINTER(ctypes.c_size_t)]),
+    "cskv_cache_reserve": (_I32, [ctypes.POINTER(ReserveArgs), _P, ctypes.c_size_t, _P]),
+    "cskv_compact_ws_bytes": (_I32, [ctypes.POINTER(CompactArgs), ctypes.POINTER(ctypes.c_size_t)]),
+    "cskv_cache_compact": (_I32, [ctypes.POINTER(CompactArgs), _P, ctypes.c_size_t, _P]),
     "csa_index_ws_bytes": (_I32, [ctypes.POINTER(IndexArgs), ctypes.POINTER(ctypes.c_size_t)]),
     "csa_index_score_topk": (_I32, [ctypes.POINTER(IndexArgs), _P, ctypes.c_size_t, _P]),
     "csa_index_score_topk_static": (_I32, [ctypes.POINTER(IndexArgs), _P]),
@@ -198,6 +233,7 @@ class Layer:
     pos_bias_idx: torch.Tensor = None
     overlap: int = 0  # block overlap: an entry also folds the last `overlap` tokens of the block before it
     _struct: LayerStruct = field(default=None, repr=False)
+    page_refs: torch.Tensor = None  # [n_pages] int32: table slots that hold each page (see track_pages)
 
     @property
     def is_csa(self) -> bool:
@@ -259,6 +295,22 @@ class Layer:
     def set_pages(self, seq: int, pages: torch.Tensor):
         """Give sequence `seq` the pool pages `pages` (int32) for its entries 0, P, 2P, ..."""
         self.page_table[seq, : pages.numel()] = pages.to(torch.int32).to(self.page_table.device)
+        if self.page_refs is not None:
+            self.track_pages()
+
+    def track_pages(self) -> torch.Tensor:
+        """Count the page-table slots that hold each page into `page_refs` (allocated on the first call).
+
+        The page operators need the counts; call it once when the table is set up, and again after the
+        table was written by anything else than they and `set_pages`."""
+        held = self.page_table.reshape(-1)
+        held = held[(held >= 0) & (held < self.n_pages)].long()
+        refs = torch.bincount(held, minlength=self.n_pages).to(torch.int32)
+        if self.page_refs is None:
+            self.page_refs = refs
+        else:
+            self.page_refs.copy_(refs)  # in place: captured calls keep its address
+        return self.page_refs
 
     def rows_of(self, seq: int, j0: int, n: int) -> torch.Tensor:
         """Pool row ids (int64) of entries j0 .. j0+n-1 of sequence `seq`."""
@@ -350,6 +402,87 @@ def cskv_cache_append(layer: Layer, seq_ids, pos, x, z, xi=None, zi=None, ring_o
     a = AppendArgs(ctypes.sizeof(AppendArgs), ctypes.pointer(layer.struct), n_seq, n_new, _ptr(seq_ids), _ptr(pos),
                    _ptr(x), _ptr(z), _ptr(xi), _ptr(zi), int(bool(ring_only)), _ptr(status), int(bool(emit_only)))
     _check(lib().cskv_cache_append(ctypes.byref(a), _stream(stream)), "cskv_cache_append")
+
+
+def _need_refs(layer: Layer):
+    if layer.page_refs is None:
+        raise ValueError("the layer's pages are not counted: call layer.track_pages() first")
+    _need(layer.page_refs, "page_refs", torch.int32, (layer.n_pages,))
+
+
+def cskv_cache_fork(layer: Layer, src_seqs, dst_seqs, n_entries, status=None, stream=None):
+    """Make each dst sequence a branch of its src: it shares the pages of the src's first n_entries entries
+    (int64 per branch) and gets a copy of the src's rings; its own pages are given back."""
+    _need_refs(layer)
+    _need(src_seqs, "src_seqs", torch.int32)
+    n = src_seqs.numel()
+    _need(src_seqs, "src_seqs", torch.int32, (n,))
+    _need(dst_seqs, "dst_seqs", torch.int32, (n,))
+    _need(n_entries, "n_entries", torch.int64, (n,))
+    _need(status, "status", torch.int32, optional=True)
+    a = ForkArgs(ctypes.sizeof(ForkArgs), ctypes.pointer(layer.struct), _ptr(layer.page_refs), n, _ptr(src_seqs),
+                 _ptr(dst_seqs), _ptr(n_entries), _ptr(status))
+    _check(lib().cskv_cache_fork(ctypes.byref(a), _stream(stream)), "cskv_cache_fork")
+
+
+def cskv_cache_free(layer: Layer, seq_ids, keep, status=None, stream=None):
+    """Give back the pages behind the first keep entries (int64 per sequence; 0: all) of each sequence."""
+    _need_refs(layer)
+    _need(seq_ids, "seq_ids", torch.int32)
+    n = seq_ids.numel()
+    _need(seq_ids, "seq_ids", torch.int32, (n,))
+    _need(keep, "keep", torch.int64, (n,))
+    _need(status, "status", torch.int32, optional=True)
+    a = FreeArgs(ctypes.sizeof(FreeArgs), ctypes.pointer(layer.struct), _ptr(layer.page_refs), n, _ptr(seq_ids),
+                 _ptr(keep), _ptr(status))
+    _check(lib().cskv_cache_free(ctypes.byref(a), _stream(stream)), "cskv_cache_free")
+
+
+def cskv_reserve_ws_bytes(layer: Layer, n_seq: int, max_count: int) -> int:
+    a = ReserveArgs(ctypes.sizeof(ReserveArgs), ctypes.pointer(layer.struct), None, n_seq, None, None, None,
+                    int(max_count), None)
+    n = ctypes.c_size_t()
+    _check(lib().cskv_reserve_ws_bytes(ctypes.byref(a), ctypes.byref(n)), "cskv_reserve_ws_bytes")
+    return n.value
+
+
+def cskv_cache_reserve(layer: Layer, seq_ids, first, count, max_count: int, workspace=None, status=None, stream=None):
+    """Make every page that entries first .. first + count - 1 of each sequence touch present and private
+    (int64 per sequence, count <= max_count): missing ones take free pages, shared ones are copied."""
+    _need_refs(layer)
+    _need(seq_ids, "seq_ids", torch.int32)
+    n = seq_ids.numel()
+    _need(seq_ids, "seq_ids", torch.int32, (n,))
+    _need(first, "first", torch.int64, (n,))
+    _need(count, "count", torch.int64, (n,))
+    _need(status, "status", torch.int32, optional=True)
+    if workspace is None:
+        workspace = torch.empty(cskv_reserve_ws_bytes(layer, n, max_count), dtype=torch.uint8, device=seq_ids.device)
+    a = ReserveArgs(ctypes.sizeof(ReserveArgs), ctypes.pointer(layer.struct), _ptr(layer.page_refs), n,
+                    _ptr(seq_ids), _ptr(first), _ptr(count), int(max_count), _ptr(status))
+    _check(lib().cskv_cache_reserve(ctypes.byref(a), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "cskv_cache_reserve")
+
+
+def cskv_compact_ws_bytes(src: Layer, dst: Layer) -> int:
+    a = CompactArgs(ctypes.sizeof(CompactArgs), ctypes.pointer(src.struct), ctypes.pointer(dst.struct), None, None, None)
+    n = ctypes.c_size_t()
+    _check(lib().cskv_compact_ws_bytes(ctypes.byref(a), ctypes.byref(n)), "cskv_compact_ws_bytes")
+    return n.value
+
+
+def cskv_cache_compact(src: Layer, dst: Layer, workspace=None, status=None, stream=None):
+    """Move src's live pages, in page order, to the front of dst's pool and give dst src's table and counts
+    with the new page ids (dst.page_refs is needed; the rings are not copied)."""
+    _need_refs(src)
+    _need_refs(dst)
+    _need(status, "status", torch.int32, optional=True)
+    if workspace is None:
+        workspace = torch.empty(cskv_compact_ws_bytes(src, dst), dtype=torch.uint8, device=src.page_table.device)
+    a = CompactArgs(ctypes.sizeof(CompactArgs), ctypes.pointer(src.struct), ctypes.pointer(dst.struct),
+                    _ptr(src.page_refs), _ptr(dst.page_refs), _ptr(status))
+    _check(lib().cskv_cache_compact(ctypes.byref(a), _ptr(workspace), workspace.numel(), _stream(stream)),
+           "cskv_cache_compact")
 
 
 def _index_args(layer, q_seq, q_pos, max_pos, q_idx, w, k, out_idx, out_cnt, out_scores, q_idx_scale, status,

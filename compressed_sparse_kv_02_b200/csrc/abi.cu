@@ -249,6 +249,74 @@ int32_t append_emit_only(const cskv_append_args* a) {
   return a->struct_size >= offsetof(cskv_append_args, emit_only) + sizeof(int32_t) ? a->emit_only : 0;
 }
 
+// Pools and rings of a layer as the page operators see them; false when a pool or the table is missing or a
+// pool is not 16-byte aligned.
+bool fill_pages(cskv::PageParams& p, const cskv_layer* L, int32_t* refs, int32_t* status) {
+  memset(&p, 0, sizeof(p));
+  const bool csa = L->kind == CSKV_LAYER_CSA;
+  const int64_t ps = L->page_size;
+  p.table = const_cast<int32_t*>(L->page_table);
+  p.refs = refs;
+  p.pool[0] = {static_cast<uint8_t*>(L->kv_pool), ps * L->d_qk * (L->kv_dtype == CSKV_BF16 ? 2 : 1)};
+  if (L->kv_dtype == CSKV_FP8_E4M3) p.pool[1] = {reinterpret_cast<uint8_t*>(L->kv_scale), ps * 4};
+  if (csa) {
+    p.pool[2] = {static_cast<uint8_t*>(L->idx_pool), L->idx_dtype == CSKV_BF16 ? ps * L->d_idx * 2 : ps * L->d_idx / 2};
+    if (L->idx_dtype == CSKV_FP4_E2M1) p.pool[3] = {L->idx_scale, ps * (L->d_idx / 16)};
+  }
+  p.n_pages = L->n_pages;
+  p.n_seqs = L->n_seqs;
+  p.max_pages = L->max_pages_per_seq;
+  p.page_size = L->page_size;
+  p.status = status;
+  for (int i = 0; i < 4; ++i)
+    if (p.pool[i].bytes && (!p.pool[i].base || !aligned16(p.pool[i].base))) return false;
+  return p.table && refs && aligned16(refs);
+}
+
+// Shape rules of the page operators: page ids are int32, and table indices are taken in 32 bits per row.
+cskv_status check_paged(const cskv_layer* L) {
+  cskv_status s = check_layer_shape(L);
+  if (s) return s;
+  return L->n_pages > 0x7fffffff ? CSKV_ERR_UNSUPPORTED : CSKV_OK;
+}
+
+cskv_status check_reserve(const cskv_reserve_args* a) {
+  if (!a || a->struct_size < sizeof(cskv_reserve_args)) return CSKV_ERR_INVALID_ARG;
+  cskv_status s = check_paged(a->layer);
+  if (s) return s;
+  if (a->n_seq < 0 || a->max_count < 0) return CSKV_ERR_INVALID_ARG;
+  const int64_t most = a->max_count / a->layer->page_size + 2;  // slots a request can touch
+  if (a->n_seq > cskv::kMaxPageSeqs || most > 0x7fffffff / cskv::kMaxPageSeqs) return CSKV_ERR_UNSUPPORTED;
+  return CSKV_OK;
+}
+
+bool reserve_params(cskv::PageParams& p, const cskv_reserve_args* a) {
+  const bool ok = fill_pages(p, a->layer, a->page_refs, a->d_status);
+  p.n = a->n_seq;
+  p.seq = a->seq_ids;
+  p.first = a->first;
+  p.count = a->count;
+  p.max_count = a->max_count;
+  return ok;
+}
+
+cskv_status check_compact(const cskv_compact_args* a) {
+  if (!a || a->struct_size < sizeof(cskv_compact_args)) return CSKV_ERR_INVALID_ARG;
+  cskv_status s = check_paged(a->src);
+  if (s || (s = check_paged(a->dst))) return s;
+  const cskv_layer &x = *a->src, &y = *a->dst;
+  if (x.kind != y.kind || x.page_size != y.page_size || x.d_qk != y.d_qk || x.kv_dtype != y.kv_dtype ||
+      x.n_seqs != y.n_seqs || y.max_pages_per_seq < x.max_pages_per_seq)
+    return CSKV_ERR_INVALID_ARG;
+  if (x.kind == CSKV_LAYER_CSA && (x.d_idx != y.d_idx || x.idx_dtype != y.idx_dtype)) return CSKV_ERR_INVALID_ARG;
+  return CSKV_OK;
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 }  // namespace
 
 extern "C" {
@@ -308,6 +376,97 @@ cskv_status cskv_cache_append(const cskv_append_args* a, void* stream) {
   p.emit_only = emit_only;
   p.status = a->d_status;
   return from_cuda(cskv::launch_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+cskv_status cskv_cache_fork(const cskv_fork_args* a, void* stream) {
+  if (!a || a->struct_size < sizeof(cskv_fork_args)) return CSKV_ERR_INVALID_ARG;
+  const cskv_layer* L = a->layer;
+  cskv_status s = check_paged(L);
+  if (s) return s;
+  if ((s = check_layer_ptrs(L))) return s;
+  if (a->n < 0) return CSKV_ERR_INVALID_ARG;
+  if (a->n > cskv::kMaxPageSeqs) return CSKV_ERR_UNSUPPORTED;
+  cskv::PageParams p;
+  if (!fill_pages(p, L, a->page_refs, a->d_status)) return CSKV_ERR_INVALID_ARG;
+  if (a->n == 0) return CSKV_OK;
+  if (!a->src_seqs || !a->dst_seqs || !a->n_entries) return CSKV_ERR_INVALID_ARG;
+  const int64_t w = L->n_win;
+  p.ring[0] = {static_cast<uint8_t*>(L->ring_x), w * L->d_qk * 2};
+  p.ring[1] = {static_cast<uint8_t*>(L->ring_z), w * L->gate_cols * 2};
+  if (L->kind == CSKV_LAYER_CSA) {
+    p.ring[2] = {static_cast<uint8_t*>(L->ring_xi), w * L->d_idx * 2};
+    p.ring[3] = {static_cast<uint8_t*>(L->ring_zi), w * L->gate_cols_idx * 2};
+  }
+  p.n = a->n;
+  p.seq = a->dst_seqs;
+  p.src = a->src_seqs;
+  p.first = a->n_entries;
+  return from_cuda(cskv::launch_fork(p, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+cskv_status cskv_cache_free(const cskv_free_args* a, void* stream) {
+  if (!a || a->struct_size < sizeof(cskv_free_args)) return CSKV_ERR_INVALID_ARG;
+  cskv_status s = check_paged(a->layer);
+  if (s) return s;
+  if (a->n_seq < 0) return CSKV_ERR_INVALID_ARG;
+  if (a->n_seq > cskv::kMaxPageSeqs) return CSKV_ERR_UNSUPPORTED;
+  if (!a->layer->page_table || !a->page_refs) return CSKV_ERR_INVALID_ARG;
+  if (a->n_seq == 0) return CSKV_OK;
+  if (!a->seq_ids || !a->keep) return CSKV_ERR_INVALID_ARG;
+  cskv::PageParams p;
+  fill_pages(p, a->layer, a->page_refs, a->d_status);  // the pools themselves are not touched
+  p.n = a->n_seq;
+  p.seq = a->seq_ids;
+  p.first = a->keep;
+  return from_cuda(cskv::launch_free(p, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+cskv_status cskv_reserve_ws_bytes(const cskv_reserve_args* a, size_t* bytes) {
+  cskv_status s = check_reserve(a);
+  if (s) return s;
+  if (!bytes) return CSKV_ERR_INVALID_ARG;
+  cskv::PageParams p;
+  reserve_params(p, a);
+  *bytes = cskv::reserve_ws_bytes(p);
+  return CSKV_OK;
+}
+
+cskv_status cskv_cache_reserve(const cskv_reserve_args* a, void* ws, size_t ws_bytes, void* stream) {
+  cskv_status s = check_reserve(a);
+  if (s) return s;
+  cskv::PageParams p;
+  if (!reserve_params(p, a)) return CSKV_ERR_INVALID_ARG;
+  if (a->n_seq == 0) return CSKV_OK;
+  if (!a->seq_ids || !a->first || !a->count) return CSKV_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < cskv::reserve_ws_bytes(p) || !aligned16(ws)) return CSKV_ERR_WORKSPACE;
+  return from_cuda(cskv::launch_reserve(p, ws, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+cskv_status cskv_compact_ws_bytes(const cskv_compact_args* a, size_t* bytes) {
+  cskv_status s = check_compact(a);
+  if (s) return s;
+  if (!bytes) return CSKV_ERR_INVALID_ARG;
+  cskv::PageParams p;
+  fill_pages(p, a->src, nullptr, nullptr);
+  *bytes = cskv::compact_ws_bytes(p);
+  return CSKV_OK;
+}
+
+cskv_status cskv_cache_compact(const cskv_compact_args* a, void* ws, size_t ws_bytes, void* stream) {
+  cskv_status s = check_compact(a);
+  if (s) return s;
+  cskv::PageParams src, dst;
+  if (!fill_pages(src, a->src, const_cast<int32_t*>(a->src_refs), a->d_status) ||
+      !fill_pages(dst, a->dst, a->dst_refs, a->d_status))
+    return CSKV_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i)
+    if (overlap(src.pool[i].base, src.pool[i].bytes * src.n_pages, dst.pool[i].base, dst.pool[i].bytes * dst.n_pages))
+      return CSKV_ERR_INVALID_ARG;
+  if (overlap(src.refs, 4 * src.n_pages, dst.refs, 4 * dst.n_pages) ||
+      overlap(src.table, (int64_t)4 * src.n_seqs * src.max_pages, dst.table, (int64_t)4 * dst.n_seqs * dst.max_pages))
+    return CSKV_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < cskv::compact_ws_bytes(src) || !aligned16(ws)) return CSKV_ERR_WORKSPACE;
+  return from_cuda(cskv::launch_compact(src, dst, ws, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 
 cskv_status csa_index_ws_bytes(const cskv_index_args* a, size_t* bytes) {
@@ -405,6 +564,7 @@ const char* cskv_status_string(cskv_status s) {
     case CSKV_ERR_CUDA: return "CUDA launch error";
     case CSKV_ERR_TIMEOUT: return "bounded device wait timed out";
     case CSKV_ERR_OUT_OF_RANGE: return "page id or index out of range on device";
+    case CSKV_ERR_NO_PAGES: return "too few free pages in the pool";
     default: return "unknown status";
   }
 }

@@ -73,6 +73,35 @@ struct FoldParams {
 cudaError_t launch_fold_bulk(const FoldParams& p, cudaStream_t st);
 cudaError_t launch_append(const FoldParams& p, cudaStream_t st);
 
+// Page operators (pages.cu).
+constexpr int kMaxPageSeqs = 4096;  // sequences one call may list
+struct PagePool {
+  uint8_t* base;   // null: the layer has no such pool
+  int64_t bytes;   // of one page (a multiple of 16)
+};
+struct PageParams {
+  int32_t* table;      // [n_seqs, max_pages]
+  int32_t* refs;       // [n_pages]
+  PagePool pool[4];    // entries, their scales, indexer keys, their scales
+  PagePool ring[4];    // x, z, xi, zi: one sequence's ring is a "page"
+  int64_t n_pages;
+  int n_seqs, max_pages, page_size;
+  int n;               // list entries
+  const int32_t* seq;  // fork: the dst sequences
+  const int32_t* src;  // fork
+  const int64_t* first;  // fork: n_entries, free: keep
+  const int64_t* count;
+  int64_t max_count;
+  int32_t* status;
+};
+cudaError_t launch_fork(const PageParams& p, int n_sm, cudaStream_t st);
+cudaError_t launch_free(const PageParams& p, int n_sm, cudaStream_t st);
+size_t reserve_ws_bytes(const PageParams& p);
+cudaError_t launch_reserve(const PageParams& p, void* ws, int n_sm, cudaStream_t st);
+// src with its refs (not written), dst with its refs
+size_t compact_ws_bytes(const PageParams& src);
+cudaError_t launch_compact(const PageParams& src, const PageParams& dst, void* ws, int n_sm, cudaStream_t st);
+
 // Lightning indexer scan (scores of every visible entry) + top-k.
 struct IndexParams {
   int n_q, n_heads_idx, d_idx, idx_dtype;

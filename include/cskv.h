@@ -75,6 +75,7 @@ typedef int32_t cskv_status;
 #define CSKV_ERR_CUDA (-4)         /* a CUDA launch or attribute call failed */
 #define CSKV_ERR_TIMEOUT (-5)      /* a bounded device wait gave up */
 #define CSKV_ERR_OUT_OF_RANGE (-6) /* the device met a page id or index outside its buffers */
+#define CSKV_ERR_NO_PAGES (-7)     /* the pool has too few free pages */
 
 /* storage dtypes */
 #define CSKV_BF16 0
@@ -227,6 +228,122 @@ typedef struct {
 } cskv_append_args;
 
 cskv_status cskv_cache_append(const cskv_append_args* args, void* stream);
+
+/*
+ * Page operators: forking, freeing, growing and compacting a layer's paged
+ * cache (10100.com article, section 5: paged KV with prefix reuse). They are the
+ * calls that change a page table on the device; the layer's page_table buffer is
+ * written although cskv_layer declares it const. All of them keep one count per
+ * page:
+ *   page_refs [n_pages] int32: how many page-table slots hold the page; 0 = free.
+ * The caller allocates the counts with the pool, zeroes them, and counts the
+ * pages that it places in the table itself. Table slots without a page hold -1.
+ * Page choices are deterministic: the lowest free page ids, in request order
+ * (sequences as listed, slots ascending), so a replayed call repeats them.
+ * Entry counts and sequence ids are device arrays; a sequence id outside the
+ * layer reports CSKV_ERR_OUT_OF_RANGE, a negative or too large entry count
+ * CSKV_ERR_INVALID_ARG, and a table slot that names no live page
+ * CSKV_ERR_OUT_OF_RANGE. Pool buffers (scales included) and page_refs must be
+ * 16-byte aligned. At most 4096 sequences per call.
+ */
+
+/*
+ * cskv_cache_fork -- sequence dst_seqs[i] becomes a branch of src_seqs[i]: it
+ * gives back its own pages, shares the src's pages that hold entries
+ * 0 .. n_entries[i] - 1 (every count + 1, its later slots -1), and gets a copy of
+ * the src's state-cache rings, which hold the last n_win tokens only: a branch
+ * starts where its src stands. No entry is copied; a later
+ * cskv_cache_reserve copies a page before it is written. A src may have many
+ * branches in one call. An entry of the list is skipped and reported
+ * (CSKV_ERR_INVALID_ARG) when its dst is also a src in the list or a dst
+ * listed twice; a src slot without a live page is reported and stays -1 in dst.
+ */
+typedef struct {
+  uint32_t struct_size;
+  const cskv_layer* layer;
+  int32_t* page_refs;
+  int32_t n;
+  const int32_t* src_seqs;  /* [n] */
+  const int32_t* dst_seqs;  /* [n] */
+  const int64_t* n_entries; /* [n] */
+  int32_t* d_status;
+} cskv_fork_args;
+
+cskv_status cskv_cache_fork(const cskv_fork_args* args, void* stream);
+
+/*
+ * cskv_cache_free -- sequence seq_ids[i] keeps the pages of its entries
+ * 0 .. keep[i] - 1 and gives back the others (their counts - 1, their slots -1).
+ * keep = 0 frees the sequence. A sequence listed twice keeps the smaller part.
+ * A bad list entry is skipped.
+ */
+typedef struct {
+  uint32_t struct_size;
+  const cskv_layer* layer;
+  int32_t* page_refs;
+  int32_t n_seq;
+  const int32_t* seq_ids; /* [n_seq] */
+  const int64_t* keep;    /* [n_seq] */
+  int32_t* d_status;
+} cskv_free_args;
+
+cskv_status cskv_cache_free(const cskv_free_args* args, void* stream);
+
+/*
+ * cskv_cache_reserve -- entries first[i] .. first[i] + count[i] - 1 of sequence
+ * seq_ids[i] are about to be written: every page they touch becomes present and
+ * private. A slot without a page takes a free page; a page with a count above 1
+ * is copied whole (all pools) into a free page, which replaces it in the slot
+ * (its count - 1). Each sequence that reserves a shared page gets its own copy,
+ * also when every holder of the page reserves it in this call (the page is then
+ * free afterwards). count[i] = 0 asks for nothing.
+ *   max_count (host): an upper bound of every count; sizes the workspace.
+ * All or nothing: when the pool has too few free pages (CSKV_ERR_NO_PAGES), a
+ * sequence is listed twice (CSKV_ERR_INVALID_ARG) or any other request is bad,
+ * the code is reported and no request of the call is carried out.
+ * Workspace: cskv_reserve_ws_bytes(), 16-byte aligned, free for other use after
+ * the call has run; two calls that may overlap need one each.
+ */
+typedef struct {
+  uint32_t struct_size;
+  const cskv_layer* layer;
+  int32_t* page_refs;
+  int32_t n_seq;
+  const int32_t* seq_ids; /* [n_seq] */
+  const int64_t* first;   /* [n_seq] */
+  const int64_t* count;   /* [n_seq] */
+  int64_t max_count;
+  int32_t* d_status;
+} cskv_reserve_args;
+
+cskv_status cskv_reserve_ws_bytes(const cskv_reserve_args* args, size_t* bytes);
+cskv_status cskv_cache_reserve(const cskv_reserve_args* args, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * cskv_cache_compact -- moves a layer's live pages (count > 0) to the front of
+ * another pool: the r-th live page of src, in page order, becomes page r of dst.
+ * dst's page table gets src's with the new ids (further columns -1), dst_refs
+ * src's counts (0 behind the last live page); dst's pages behind the last live
+ * one, both layers' rings and src are left as they are. For a caller that
+ * shrinks, grows or moves a pool: src and dst agree in everything but n_pages
+ * and max_pages_per_seq and share no buffer but the rings and biases, and
+ * dst.max_pages_per_seq is at least src's.
+ * When dst holds fewer pages than src has live ones, CSKV_ERR_NO_PAGES is
+ * reported and nothing is written. A table slot that names no live page is
+ * reported and becomes -1.
+ * Workspace: cskv_compact_ws_bytes(), 16-byte aligned.
+ */
+typedef struct {
+  uint32_t struct_size;
+  const cskv_layer* src;
+  const cskv_layer* dst;
+  const int32_t* src_refs;
+  int32_t* dst_refs;
+  int32_t* d_status;
+} cskv_compact_args;
+
+cskv_status cskv_compact_ws_bytes(const cskv_compact_args* args, size_t* bytes);
+cskv_status cskv_cache_compact(const cskv_compact_args* args, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * csa_index_score_topk -- Lightning-indexer scores of every visible entry
