@@ -171,16 +171,18 @@ def _check(code: int, where: str):
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: a torch Stream object per call would cost 3 us
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
 def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=False):
+    if t is not None and t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
     if t is None:
         if optional:
             return
@@ -196,6 +198,7 @@ def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=Fals
 
 
 # ------------------------------------------------------------- layer state
+_LAYER_SIZE = ctypes.sizeof(LayerStruct)
 _TORCH_STORE = {BF16: torch.bfloat16, FP8_E4M3: torch.uint8, FP4_E2M1: torch.uint8}
 
 
@@ -240,11 +243,10 @@ class Layer:
         return self.kind == LAYER_CSA
 
     def shape_struct(self) -> LayerStruct:
-        s = LayerStruct()
-        s.struct_size = ctypes.sizeof(LayerStruct)
-        for f in ("kind", "m", "n_win", "d_qk", "d_v", "d_idx", "page_size", "kv_dtype", "idx_dtype",
-                  "gate_cols", "gate_cols_idx", "n_seqs", "max_pages_per_seq", "n_pages", "overlap"):
-            setattr(s, f, int(getattr(self, f)))
+        s = LayerStruct(_LAYER_SIZE, self.kind, self.m, self.n_win, self.d_qk, self.d_v, self.d_idx, self.page_size,
+                        self.kv_dtype, self.idx_dtype, self.gate_cols, self.gate_cols_idx, self.n_seqs,
+                        self.max_pages_per_seq, self.n_pages)
+        s.overlap = self.overlap
         return s
 
     def buffer_bytes(self) -> dict:
@@ -348,11 +350,14 @@ class Layer:
 
     @property
     def struct(self) -> LayerStruct:
-        s = self.shape_struct()
-        for f in ("page_table", "kv_pool", "kv_scale", "idx_pool", "idx_scale", "ring_x", "ring_z",
-                  "ring_xi", "ring_zi", "pos_bias", "pos_bias_idx"):
-            t = getattr(self, f)
-            setattr(s, f, None if t is None else t.data_ptr())
+        # positional: one call instead of a setattr per field
+        s = LayerStruct(_LAYER_SIZE, self.kind, self.m, self.n_win, self.d_qk, self.d_v, self.d_idx, self.page_size,
+                        self.kv_dtype, self.idx_dtype, self.gate_cols, self.gate_cols_idx, self.n_seqs,
+                        self.max_pages_per_seq, self.n_pages, *[
+                            None if t is None else t.data_ptr()
+                            for t in (self.page_table, self.kv_pool, self.kv_scale, self.idx_pool, self.idx_scale,
+                                      self.ring_x, self.ring_z, self.ring_xi, self.ring_zi, self.pos_bias,
+                                      self.pos_bias_idx)], self.overlap)
         self._struct = s  # keep alive while the call runs
         return s
 
@@ -408,6 +413,8 @@ def _need_refs(layer: Layer):
     if layer.page_refs is None:
         raise ValueError("the layer's pages are not counted: call layer.track_pages() first")
     _need(layer.page_refs, "page_refs", torch.int32, (layer.n_pages,))
+    if layer.page_refs.get_device() != torch.cuda.current_device():
+        raise ValueError("the layer is on another device than the current one")
 
 
 def cskv_cache_fork(layer: Layer, src_seqs, dst_seqs, n_entries, status=None, stream=None):

@@ -202,8 +202,7 @@ ReserveWs reserve_ws(const PageParams& p, void* ws) {
 // pages. Nothing but the workspace is written: the counts must not change while other CTAs rank them.
 __global__ void __launch_bounds__(kRankThreads) reserve_plan_kernel(PageParams p, ReserveWs w) {
   __shared__ int s_warp[32];
-  __shared__ int s_seq[kMaxPageSeqs];
-  __shared__ int s_pre[kMaxPageSeqs + 1];  // touched slots before each request
+  extern __shared__ int s_req[];  // [n] sequences | [n] first slots | [n + 1] touched slots before each request
   grid_dependency_wait();
   grid_dependents_launch();
   const int tid = threadIdx.x;
@@ -221,56 +220,72 @@ __global__ void __launch_bounds__(kRankThreads) reserve_plan_kernel(PageParams p
     if (blockIdx.x == gridDim.x - 1 && tid == 0) w.head[1] = sum;
     return;
   }
+  int* s_seq = s_req;
+  int* s_slot = s_seq + p.n;  // a request's first slot minus the touched slots before it
+  int* s_pre = s_slot + p.n;
   int code = 0, run = 0;
-  for (int i = tid; i < p.n; i += kRankThreads) s_seq[i] = p.seq[i];
-  __syncthreads();
   for (int base = 0; base < p.n; base += kRankThreads) {
     const int i = base + tid;
-    int touched = 0;
+    int touched = 0, k0 = 0;
     if (i < p.n) {
-      const int seq = s_seq[i];
+      const int seq = p.seq[i];
       const int64_t first = p.first[i], count = p.count[i], end = (int64_t)p.max_pages * p.page_size;
-      if (seq < 0 || seq >= p.n_seqs)
+      if (seq < 0 || seq >= p.n_seqs) {
         code = CSKV_ERR_OUT_OF_RANGE;
-      else if (first < 0 || count < 0 || count > p.max_count || first > end || first + count > end)
+      } else if (first < 0 || count < 0 || count > p.max_count || first > end || first + count > end) {
         code = CSKV_ERR_INVALID_ARG;
-      else if (count > 0)
-        touched = static_cast<int>((first + count - 1) / p.page_size - first / p.page_size + 1);
-      for (int j = 0; j < i; ++j)
-        if (s_seq[j] == seq) code = CSKV_ERR_INVALID_ARG;  // listed twice
+      } else if (count > 0) {
+        k0 = static_cast<int>(first / p.page_size);
+        touched = static_cast<int>((first + count - 1) / p.page_size) - k0 + 1;
+      }
+      s_seq[i] = seq;
     }
     int tot;
     const int ex = block_exclusive_scan<kRankThreads>(touched, s_warp, tot);
-    if (i < p.n) s_pre[i] = run + ex;
+    if (i < p.n) {
+      s_pre[i] = run + ex;
+      s_slot[i] = k0 - (run + ex);
+    }
     run += tot;
+  }
+  __syncthreads();
+  for (int f = tid; f < p.n * p.n; f += kRankThreads) {
+    const int i = f / p.n, j = f % p.n;
+    if (j < i && s_seq[j] == s_seq[i]) code = CSKV_ERR_INVALID_ARG;  // listed twice
   }
   if (tid == 0) s_pre[p.n] = run;
   int need = 0, n_cow = 0;
   if (!__syncthreads_or(code != 0)) {
     for (int64_t base = 0; base < run; base += kChunk) {
-      int4 slot[4];
+      // four slots per thread; the loads of all four are issued before any is used
+      int seq[4], k[4];
+      int32_t page[4], refs[4];
+      int lo = 0, hi = p.n - 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int f = static_cast<int>(base + 4 * tid + j < run ? base + 4 * tid + j : run - 1);
+        while (j == 0 && lo < hi) {  // the request of the thread's first slot; the others follow on
+          const int mid = (lo + hi + 1) >> 1;
+          if (s_pre[mid] <= f) lo = mid; else hi = mid - 1;
+        }
+        while (s_pre[lo + 1] <= f) ++lo;
+        seq[j] = s_seq[lo];
+        k[j] = f + s_slot[lo];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) page[j] = p.table[(int64_t)seq[j] * p.max_pages + k[j]];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) refs[j] = page[j] >= 0 && page[j] < p.n_pages ? p.refs[page[j]] : 0;
       int flags = 0;  // needs a new page in the low half, copies one in the high half
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int64_t f = base + 4 * tid + j;
-        slot[j] = make_int4(-1, 0, -1, 0);
-        if (f < run) {
-          int lo = 0, hi = p.n - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_pre[mid] <= f) lo = mid; else hi = mid - 1;
-          }
-          const int k = static_cast<int>(p.first[lo] / p.page_size + (f - s_pre[lo]));
-          const int32_t page = p.table[(int64_t)s_seq[lo] * p.max_pages + k];
-          if (page < 0) {
-            slot[j] = make_int4(s_seq[lo], k, -1, 0);
-            flags += 1;
-          } else if (!live_page(p, page)) {
-            code = CSKV_ERR_OUT_OF_RANGE;
-          } else if (p.refs[page] > 1) {
-            slot[j] = make_int4(s_seq[lo], k, page, 0);
-            flags += 1 + (1 << 16);
-          }
+        if (base + 4 * tid + j >= run || (page[j] >= 0 && refs[j] == 1)) {
+          seq[j] = -1;  // nothing to do
+        } else if (page[j] >= 0 && refs[j] <= 0) {
+          seq[j] = -1;
+          code = CSKV_ERR_OUT_OF_RANGE;
+        } else {
+          flags += page[j] >= 0 ? 1 + (1 << 16) : 1;
         }
       }
       int tot;
@@ -278,12 +293,12 @@ __global__ void __launch_bounds__(kRankThreads) reserve_plan_kernel(PageParams p
       int r = need + (ex & 0xffff), c = n_cow + (ex >> 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (slot[j].x >= 0) {
+        if (seq[j] >= 0) {
           if (r < w.cap) {
-            w.slot[r] = slot[j];
-            if (slot[j].z >= 0) w.cow[c] = r;
+            w.slot[r] = make_int4(seq[j], k[j], page[j] >= 0 ? page[j] : -1, 0);
+            if (page[j] >= 0) w.cow[c] = r;
           }
-          c += slot[j].z >= 0;
+          c += page[j] >= 0;
           ++r;
         }
       need += tot & 0xffff;
@@ -292,14 +307,14 @@ __global__ void __launch_bounds__(kRankThreads) reserve_plan_kernel(PageParams p
   }
   // one code for the call: the first thread that has one names it
   __syncthreads();
-  if (tid == 0) s_pre[0] = 0;
+  if (tid == 0) s_warp[0] = 0;
   __syncthreads();
-  if (code) atomicCAS(&s_pre[0], 0, code);
+  if (code) atomicCAS(&s_warp[0], 0, code);
   __syncthreads();
   if (tid == 0) {
     w.head[0] = need;
     w.head[2] = n_cow;
-    w.head[3] = s_pre[0];
+    w.head[3] = s_warp[0];
   }
 }
 
@@ -409,7 +424,12 @@ size_t reserve_ws_bytes(const PageParams& p) { return kHeadBytes + static_cast<s
 
 cudaError_t launch_reserve(const PageParams& p, void* ws, int n_sm, cudaStream_t st) {
   const ReserveWs w = reserve_ws(p, ws);
-  cudaError_t e = launch_pdl(reserve_plan_kernel, dim3(1 + rank_ctas(p.n_pages)), dim3(kRankThreads), 0, st, p, w);
+  const size_t smem = sizeof(int) * (3 * (size_t)p.n + 1);
+  cudaError_t e = cudaSuccess;
+  if (smem > 40000)  // the static default is 48 KB, the kernel's own arrays included
+    e = cudaFuncSetAttribute(reserve_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(reserve_plan_kernel, dim3(1 + rank_ctas(p.n_pages)), dim3(kRankThreads), smem, st, p, w);
   if (e != cudaSuccess) return e;
   int64_t grid = w.cap * slices_of(p.pool);
   if (grid > 4 * n_sm) grid = 4 * n_sm;

@@ -212,6 +212,18 @@ def test_many_pages_and_sequences(ck):
     b.reserve(seqs[:4], [17500, 0, 16999, 5], [100, 16 * 40, 16, 11], most=16 * 40)
 
 
+def test_the_longest_list(ck):
+    """4096 sequences in one call, and one of them listed twice."""
+    L = make(ck, kind="hca", m=128, d=16, d_v=16, gate=1, n_win=128, page_size=16, n_seqs=4097, n_pages=4200, max_pages=2)
+    b = Both(ck, L)
+    seqs = np.random.default_rng(2).permutation(4097)[:4096].tolist()
+    b.reserve(seqs, [0] * 4096, [1] * 4096)
+    b.free(seqs, [0] * 4096)
+    seqs[4095] = seqs[17]
+    _refused(ck, b, ck.ERR_INVALID_ARG,
+             lambda: ck.cskv_cache_reserve(L, i32(seqs), i64([0] * 4096), i64([1] * 4096), 1, status=b.status))
+
+
 def test_no_pages_changes_nothing(ck):
     L = make(ck, n_seqs=4, n_pages=5, max_pages=4)
     b = Both(ck, L)
