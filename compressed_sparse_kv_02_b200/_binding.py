@@ -87,7 +87,8 @@ class AttendArgs(ctypes.Structure):
         ("n_heads", _I32), ("q_seq", _P), ("q_pos", _P), ("max_pos", _I64), ("q", _P),
         ("sel_idx", _P), ("sel_cnt", _P), ("k", _I32), ("sm_scale", ctypes.c_float), ("out", _P),
         ("lse", _P), ("x_chunk", _P), ("chunk_pos0", _I64), ("chunk_len", _I64), ("d_status", _P),
-        ("rope_dims", _I32), ("rope_base", ctypes.c_float), ("chunk_desc", _P),
+        ("rope_dims", _I32), ("rope_base", ctypes.c_float), ("chunk_desc", _P), ("score_cap", ctypes.c_float),
+        ("slopes", _P),
     ]
 
 
@@ -559,7 +560,8 @@ def csa_index_score_topk_static(layer: Layer, q_seq, q_pos, max_pos: int, q_idx,
 
 
 def _attend_args(layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, sm_scale, out, lse, x_chunk, chunk_pos0,
-                 status, n_q=None, n_heads=None, rope_dims=0, rope_base=10000.0, chunk_desc=None):
+                 status, n_q=None, n_heads=None, rope_dims=0, rope_base=10000.0, chunk_desc=None, score_cap=0.0,
+                 slopes=None):
     if q is not None:
         n_q, n_heads = q.shape[0], q.shape[1]
     if sm_scale is None:
@@ -568,7 +570,7 @@ def _attend_args(layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, sm_scale,
                       _ptr(q_pos), int(max_pos), _ptr(q), _ptr(sel_idx), _ptr(sel_cnt), int(k), float(sm_scale),
                       _ptr(out), _ptr(lse), _ptr(x_chunk), int(chunk_pos0),
                       0 if x_chunk is None else int(x_chunk.shape[0]), _ptr(status), int(rope_dims),
-                      float(rope_base), _ptr(chunk_desc))
+                      float(rope_base), _ptr(chunk_desc), float(score_cap), _ptr(slopes))
 
 
 def cskv_attend_ws_bytes(layer: Layer, n_q: int, n_heads: int, max_pos: int, k: int = 0) -> int:
@@ -579,8 +581,9 @@ def cskv_attend_ws_bytes(layer: Layer, n_q: int, n_heads: int, max_pos: int, k: 
 
 
 def _attend(fn, where, layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, out, lse, sm_scale, workspace,
-            x_chunk, chunk_pos0, status, stream, rope_dims=0, rope_base=10000.0):
+            x_chunk, chunk_pos0, status, stream, rope_dims=0, rope_base=10000.0, score_cap=0.0, slopes=None):
     n_q, n_heads = q.shape[0], q.shape[1]
+    _need(slopes, "slopes", torch.float32, (n_heads,), optional=True)
     _need(q_seq, "q_seq", torch.int32, (n_q,))
     _need(q_pos, "q_pos", torch.int64, (n_q,))
     _need(q, "q", torch.bfloat16, (n_q, n_heads, layer.d_qk))
@@ -592,33 +595,35 @@ def _attend(fn, where, layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, out
         workspace = torch.empty(cskv_attend_ws_bytes(layer, n_q, n_heads, max_pos, k), dtype=torch.uint8,
                                 device=q.device)
     a = _attend_args(layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, sm_scale, out, lse, x_chunk, chunk_pos0,
-                     status, rope_dims=rope_dims, rope_base=rope_base)
+                     status, rope_dims=rope_dims, rope_base=rope_base, score_cap=score_cap, slopes=slopes)
     _check(fn(ctypes.byref(a), _ptr(workspace), workspace.numel(), _stream(stream)), where)
 
 
 def csa_attend(layer: Layer, q_seq, q_pos, max_pos: int, q, sel_idx, sel_cnt, out, lse=None, sm_scale=None,
                workspace=None, x_chunk=None, chunk_pos0: int = 0, status=None, stream=None, rope_dims: int = 0,
-               rope_base: float = 10000.0):
+               rope_base: float = 10000.0, score_cap: float = 0.0, slopes=None):
     """One softmax over the window and the selected CSA entries, every head sharing the latent KV
-    (rope_dims > 0: inverse RoPE on the output's last rope_dims channels at each query's position)."""
+    (rope_dims > 0: inverse RoPE on the output's last rope_dims channels at each query's position;
+    score_cap > 0: logits capped by a tanh; slopes [n_heads] fp32: a bias of -slope per token of distance)."""
     if not layer.is_csa:
         raise ValueError("csa_attend needs a CSA layer")
     k = sel_idx.shape[1]
     _need(sel_idx, "sel_idx", torch.int32, (q.shape[0], k))
     _need(sel_cnt, "sel_cnt", torch.int32, (q.shape[0],))
     _attend(lib().csa_attend, "csa_attend", layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, out, lse,
-            sm_scale, workspace, x_chunk, chunk_pos0, status, stream, rope_dims, rope_base)
+            sm_scale, workspace, x_chunk, chunk_pos0, status, stream, rope_dims, rope_base, score_cap, slopes)
 
 
 def hca_attend(layer: Layer, q_seq, q_pos, max_pos: int, q, out, lse=None, sm_scale=None, workspace=None,
                x_chunk=None, chunk_pos0: int = 0, status=None, stream=None, rope_dims: int = 0,
-               rope_base: float = 10000.0):
+               rope_base: float = 10000.0, score_cap: float = 0.0, slopes=None):
     """One softmax over the window and every visible HCA entry (rope_dims > 0: inverse RoPE on the
-    output's last rope_dims channels at each query's position)."""
+    output's last rope_dims channels at each query's position; score_cap > 0: logits capped by a tanh;
+    slopes [n_heads] fp32: a bias of -slope per token of distance)."""
     if layer.is_csa:
         raise ValueError("hca_attend needs an HCA layer")
     _attend(lib().hca_attend, "hca_attend", layer, q_seq, q_pos, max_pos, q, None, None, 0, out, lse, sm_scale,
-            workspace, x_chunk, chunk_pos0, status, stream, rope_dims, rope_base)
+            workspace, x_chunk, chunk_pos0, status, stream, rope_dims, rope_base, score_cap, slopes)
 
 
 def cskv_get_status(status: torch.Tensor, stream=None) -> int:

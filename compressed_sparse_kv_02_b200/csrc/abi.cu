@@ -169,6 +169,11 @@ int32_t attend_rope_dims(const cskv_attend_args* a) {
   return a->struct_size >= offsetof(cskv_attend_args, rope_base) + sizeof(float) ? a->rope_dims : 0;
 }
 
+// the score rule of the args (none for callers whose struct_size ends before it)
+bool has_rule_fields(const cskv_attend_args* a) {
+  return a->struct_size >= offsetof(cskv_attend_args, slopes) + sizeof(float*);
+}
+
 cskv_status check_attend(const cskv_attend_args* a, int kind) {
   if (!a || a->struct_size < kAttendArgsV1) return CSKV_ERR_INVALID_ARG;
   {
@@ -176,6 +181,8 @@ cskv_status check_attend(const cskv_attend_args* a, int kind) {
     if (rd < 0 || rd % 2 || (a->layer && rd > a->layer->d_v) || (rd > 0 && !(a->rope_base > 0.f)))
       return CSKV_ERR_INVALID_ARG;
   }
+  if (has_rule_fields(a) && a->score_cap != 0.f && !(a->score_cap >= 0x1p-100f && a->score_cap <= 0x1p100f))
+    return CSKV_ERR_INVALID_ARG;
   const cskv_layer* L = a->layer;
   cskv_status s = check_layer_shape(L);
   if (s) return s;
@@ -223,6 +230,10 @@ void fill_attend(AttendParams& p, const cskv_attend_args* a, int kind) {
   p.status = a->d_status;
   p.rope_dims = attend_rope_dims(a);
   p.rope_base = p.rope_dims > 0 ? a->rope_base : 0.f;
+  if (has_rule_fields(a)) {
+    p.score_cap = a->score_cap;
+    p.slopes = a->slopes;
+  }
   p.chunk_desc = a->struct_size >= offsetof(cskv_attend_args, chunk_desc) + sizeof(void*) ? a->chunk_desc : nullptr;
 }
 

@@ -17,9 +17,12 @@
 // writes the split's normalised partial output and log-sum-exp; a merge
 // kernel combines the splits (log-sum-exp weighting) into bf16 output.
 // FP8 entries are staged as bytes, widened to bf16 in shared memory (exact),
-// and their per-entry scale is applied to the logits and to P.
+// and their per-entry scale is applied to the logits and to P. RULE is the form
+// with a cap or a distance bias on the logits: each key's distance stands beside
+// its row, and the rule is applied to the fp32 logit before the online softmax.
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
+#include "score_rule.cuh"
 
 namespace cskv {
 namespace {
@@ -61,10 +64,11 @@ __device__ __forceinline__ QueryKeys query_keys(const AttendParams& p, int b) {
 // source row of key u of query b; bit 0 of the returned address flags an FP8
 // entry (all rows are 16-byte aligned). Returns 0 for an invalid row.
 __device__ __forceinline__ uintptr_t key_row(const AttendParams& p, int b, int seq,
-                                             const QueryKeys& qk, int64_t u, float& scale) {
+                                             const QueryKeys& qk, int64_t u, float& scale, float& dist) {
   scale = 1.f;
   if (u < qk.n_w) {
     const int64_t pos = qk.ws + u;
+    dist = static_cast<float>(qk.t - pos);
     const int64_t cr = chunk_row(p, seq, pos);
     if (cr >= 0) return reinterpret_cast<uintptr_t>(p.x_chunk + cr * p.d_qk);
     return reinterpret_cast<uintptr_t>(p.ring_x + ((int64_t)seq * p.n_win + pos % p.n_win) * p.d_qk);
@@ -73,6 +77,7 @@ __device__ __forceinline__ uintptr_t key_row(const AttendParams& p, int b, int s
   const int64_t j = p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k + jj]) : jj;
   const int64_t nvis = visible_entries(qk.t, p.m, p.n_win);
   if (j < 0 || j >= nvis) return 0;
+  dist = entry_distance(qk.t, j, p.m);
   const int64_t pi = j / p.page_size;
   if (pi >= p.max_pages_per_seq) return 0;
   const int32_t page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
@@ -89,16 +94,16 @@ template <int DQK, int MT>
 struct AttnSmem {
   static constexpr int SROW = DQK + 8;  // padded row: ldmatrix rows fall in distinct banks
   static constexpr int HG = 16 * MT;
-  static size_t bytes(int n_q, int kps, bool fp8) {
+  static size_t bytes(int n_q, int kps, bool fp8, bool rule) {
     size_t s = sizeof(uint16_t) * (size_t)(HG + 2 * KT) * SROW;
     if (fp8) s += (size_t)2 * KT * DQK;
-    s += (sizeof(uintptr_t) + sizeof(float)) * (size_t)kps;
+    s += (sizeof(uintptr_t) + sizeof(float) * (rule ? 2 : 1)) * (size_t)kps;
     s += sizeof(int) * (size_t)(n_q + 1);
     return s;
   }
 };
 
-template <int DQK, int DV, int MT, int VS, bool FP8>
+template <int DQK, int DV, int MT, int VS, bool FP8, bool RULE>
 __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
   constexpr int NW = MT * VS, NTH = 32 * NW;
   constexpr int HG = 16 * MT, DVW = DV / VS;
@@ -114,7 +119,8 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
   uint8_t* sK8 = reinterpret_cast<uint8_t*>(sK + 2 * KT * SROW);  // [2][KT][DQK] (FP8)
   uintptr_t* sPtr = reinterpret_cast<uintptr_t*>(sK8 + (FP8 ? 2 * KT * DQK : 0));
   float* sSc = reinterpret_cast<float*>(sPtr + p.keys_per_split);
-  int* sPref = reinterpret_cast<int*>(sSc + p.keys_per_split);
+  float* sDist = sSc + p.keys_per_split;  // RULE: each key's distance
+  int* sPref = reinterpret_cast<int*>(sDist + (RULE ? p.keys_per_split : 0));
   __shared__ int s_wsum[32];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -162,11 +168,12 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
     const bool seq_ok = seq >= 0 && seq < p.n_seqs_layer;
 
     for (int i = tid; i < nk; i += NTH) {
-      float sc = 1.f;
-      uintptr_t a = seq_ok ? key_row(p, b, seq, qk, u0 + i, sc) : 0;
+      float sc = 1.f, dist = 0.f;
+      uintptr_t a = seq_ok ? key_row(p, b, seq, qk, u0 + i, sc, dist) : 0;
       if (a == 0) report(p.status, CSKV_ERR_OUT_OF_RANGE);
       sPtr[i] = a;
       sSc[i] = sc;
+      if (RULE) sDist[i] = dist;
     }
     for (int id = tid; id < HG * CPR; id += NTH) {
       const int rr = id / CPR, ch = id % CPR;
@@ -201,7 +208,13 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
 #pragma unroll
     for (int i = 0; i < DVW / 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
     uint32_t qa[HOIST_Q ? DQK / 16 : 1][4];
-    const float sl2 = p.sm_scale * kLog2e;
+    const bool cap = RULE && p.score_cap > 0.f;
+    const float sl2 = cap ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
+    float slope2[2] = {0.f, 0.f};
+    if (RULE && p.slopes) {
+      slope2[0] = p.slopes[grp * HG + mt * 16 + g] * kLog2e;
+      slope2[1] = p.slopes[grp * HG + mt * 16 + g + 8] * kLog2e;
+    }
 
     for (int it = 0; it < ntiles; ++it) {
       const int buf = it & 1;
@@ -263,7 +276,15 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
         for (int e = 0; e < 4; ++e) {
           const int i = it * KT + nt * 8 + 2 * c + (e & 1);
           float v = -INFINITY;  // keys past the split or without a valid row are masked
-          if (i < nk && sPtr[i] != 0) v = sacc[nt][e] * sl2 * (FP8 ? sSc[i] : 1.f);
+          if (i < nk && sPtr[i] != 0) {
+            const float sc = FP8 ? sSc[i] : 1.f;
+            if (!RULE)
+              v = sacc[nt][e] * sl2 * sc;
+            else if (cap)
+              v = ruled_score<true>(sacc[nt][e] * sc, sl2, p.score_cap * kLog2e, slope2[e >> 1], sDist[i]);
+            else
+              v = ruled_score<false>(sacc[nt][e] * sc, sl2, 0.f, slope2[e >> 1], sDist[i]);
+          }
           pr[nt][e] = v;
           mx[e >> 1] = fmaxf(mx[e >> 1], v);
         }
@@ -472,10 +493,10 @@ struct Plan {
   int mt, vs;
 };
 
-template <int DQK, int DV, int MT, int VS, bool FP8>
-cudaError_t run_attend(AttendParams& p, int n_sm, cudaStream_t st) {
-  auto kern = attend_kernel<DQK, DV, MT, VS, FP8>;
-  const size_t smem = AttnSmem<DQK, MT>::bytes(p.n_q, p.keys_per_split, FP8);
+template <int DQK, int DV, int MT, int VS, bool FP8, bool RULE>
+cudaError_t run_attend_form(AttendParams& p, int n_sm, cudaStream_t st) {
+  auto kern = attend_kernel<DQK, DV, MT, VS, FP8, RULE>;
+  const size_t smem = AttnSmem<DQK, MT>::bytes(p.n_q, p.keys_per_split, FP8, RULE);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   int per_sm = 0;
@@ -491,6 +512,12 @@ cudaError_t run_attend(AttendParams& p, int n_sm, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_attend_merge(p, st);
+}
+
+template <int DQK, int DV, int MT, int VS, bool FP8>
+cudaError_t run_attend(AttendParams& p, int n_sm, cudaStream_t st) {
+  return has_score_rule(p) ? run_attend_form<DQK, DV, MT, VS, FP8, true>(p, n_sm, st)
+                           : run_attend_form<DQK, DV, MT, VS, FP8, false>(p, n_sm, st);
 }
 
 // heads per CTA for each supported shape
@@ -544,18 +571,26 @@ static void choose_split(AttendParams& p, int n_sm) {
   if (p.max_splits < 1) p.max_splits = 1;
 }
 
-size_t attend_ws_bytes(const AttendParams& p0, int n_sm) {
-  AttendParams p = p0;
-  if (attend_tc_supported(p.d_qk, p.d_v, p.n_heads, p.kv_dtype, p.n_q))
-    attend_tc_plan(p, n_sm);
-  else
-    choose_split(p, n_sm);
+static size_t plan_bytes(const AttendParams& p) {
   const size_t rows = (size_t)p.n_q * p.max_splits * p.n_heads;
   return rows * p.d_v * sizeof(float) + rows * sizeof(float) + 256;
 }
 
+// The query takes no score rule, so it covers both forms: the larger of the plans where they differ.
+size_t attend_ws_bytes(const AttendParams& p0, int n_sm) {
+  AttendParams p = p0;
+  size_t bytes = 0;
+  if (attend_tc_supported(p.d_qk, p.d_v, p.n_heads, p.kv_dtype, p.n_q, false)) {
+    attend_tc_plan(p, n_sm);
+    bytes = plan_bytes(p);
+    if (attend_tc_supported(p.d_qk, p.d_v, p.n_heads, p.kv_dtype, p.n_q, true)) return bytes;
+  }
+  choose_split(p, n_sm);
+  return bytes > plan_bytes(p) ? bytes : plan_bytes(p);
+}
+
 cudaError_t launch_attend(AttendParams& p, void* ws, int n_sm, cudaStream_t st) {
-  const bool tc = attend_tc_supported(p.d_qk, p.d_v, p.n_heads, p.kv_dtype, p.n_q);
+  const bool tc = attend_tc_supported(p.d_qk, p.d_v, p.n_heads, p.kv_dtype, p.n_q, has_score_rule(p));
   if (tc)
     attend_tc_plan(p, n_sm);
   else

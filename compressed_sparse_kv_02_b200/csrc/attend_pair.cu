@@ -25,12 +25,18 @@
 // O is rescaled only when a row's running max rises by more than 2^8, so most
 // tiles skip it (the probabilities stay below 256 in bf16).
 //
+// RULE is the form with a cap or a distance bias on the logits: the loaders write
+// each key's distance from each query beside the valid-key bits, and the softmax
+// applies the rule once and keeps the 64 ruled logits in registers for its
+// exponentials (the plain form reads S twice instead).
+//
 // Shared memory (1024-aligned): Q 32 KB | key stages 4 x 32 KB | P 2 x 16 KB |
 // source-row codes | barriers | valid-key bits. Tensor memory: O 128 | S 2 x 64
 // columns. A key without a valid source row (an index outside the
 // visible entries) is masked out of the softmax and reported.
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
+#include "score_rule.cuh"
 
 namespace cskv {
 namespace {
@@ -63,7 +69,8 @@ struct Smem {
   static constexpr int TMEM = BAR + (2 * kNS + 9) * 8;
   static constexpr int FLAGS = TMEM + 4;
   static constexpr int MASK = FLAGS + 8;          // valid-key bits: [stage][query][2 words]
-  static constexpr int END = MASK + kNS * 2 * 2 * 4;
+  static constexpr int DIST = MASK + kNS * 2 * 2 * 4;  // RULE: distances [stage][query][64 keys]
+  static constexpr int END = DIST + kNS * 2 * kNk * 4;
   static constexpr size_t bytes() { return 1024 + END; }
 };
 static_assert(Smem::bytes() <= 232448, "shared memory budget");
@@ -101,10 +108,17 @@ __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
 // Code of the source row of key u (< k.n) of query b: window keys first (ring-slot order when
 // every window row is in the ring, position order when a prefill chunk supplies some), then the
 // compressed entries. 0 if the row is invalid.
-__device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int seq, const Keys& k, int u) {
+// dist: the key's distance from position k.t in tokens (RULE).
+__device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int seq, const Keys& k, int u,
+                                             float& dist) {
+  dist = 0.f;
   if (u < k.n_w) {
-    if (!p.x_chunk) return (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + u);
+    if (!p.x_chunk) {
+      dist = static_cast<float>((k.t - u) % p.n_win);  // slot u holds the latest position up to t that is u mod n_win
+      return (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + u);
+    }
     const int64_t pos = k.ws + u;
+    dist = static_cast<float>(k.t - pos);
     const int64_t cr = chunk_row(p, seq, pos);
     if (cr >= 0) return (3u << kRowBits) | static_cast<uint32_t>(cr);
     return (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + pos % p.n_win);
@@ -112,6 +126,7 @@ __device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int s
   const int jj = u - k.n_w;
   const int64_t j = p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k + jj]) : jj;
   if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return 0;
+  dist = entry_distance(k.t, j, p.m);
   const int64_t pi = j / p.page_size;
   if (pi >= p.max_pages_per_seq) return 0;
   const int32_t page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
@@ -157,6 +172,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pm, uint32_t v, ui
 //   softmax : wait sfull, kfull (valid-key bits) -> row max -> wait obar (P V of tile gt - 2
 //             done: P buffer free)
 //             -> rescale O if needed (after P V of gt - 1) -> P(gt) -> arrive pfull
+template <bool RULE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_pair_kernel(const __grid_constant__ CUtensorMap tm_q, AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -178,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
   volatile int* sLdOk = sAbort + 1;
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
+  float* sDist = reinterpret_cast<float*>(sm + Smem::DIST);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -272,28 +289,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // for its stage.
       const int chunk = lt & 15, half = chunk >> 3, c8 = chunk & 7;
       const int my_slot = lt >> 6, my_key = lt & (kNk - 1);
-      auto code_of = [&](int it) -> uint32_t {
+      auto code_of = [&](int it, float& di) -> uint32_t {
         uint32_t c = 0;
+        di = 0.f;
         if (shared) {  // threads 0 .. kNk - 1: key lt of the shared list
           const int u = it * kNk + lt;
           if (lt < kNk && u < ksh.n) {
-            c = key_code(p, b1, s1, ksh, u);
+            c = key_code(p, b1, s1, ksh, u, di);
             if (!c) report(p.status, CSKV_ERR_OUT_OF_RANGE);
           }
           return c;
         }
         const int u = it * kNk + my_key;
         if (u < (my_slot ? n1 : n0)) {
-          c = my_slot ? key_code(p, b1, s1, k1, u) : key_code(p, b0, s0, k0, u);
+          c = my_slot ? key_code(p, b1, s1, k1, u, di) : key_code(p, b0, s0, k0, u, di);
           if (!c) report(p.status, CSKV_ERR_OUT_OF_RANGE);
         }
         return c;
       };
-      uint32_t nc = ntiles > 0 ? code_of(0) : 0u;
+      float nd = 0.f;
+      uint32_t nc = ntiles > 0 ? code_of(0, nd) : 0u;
       for (int it = 0; it < ntiles; ++it) {
         const uint32_t gt = g + it;
         const int st = gt % kNS;
         const uint32_t c = nc;
+        const float di = nd;
         if (lw == 0) {
           bool okw = __shfl_sync(kFull, *sAbort, 0) == 0;
           if (okw && gt >= (uint32_t)kNS)
@@ -306,6 +326,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         sRow[lt] = c;
+        if (RULE) {
+          if (!shared) {
+            sDist[st * kRows + lt] = di;
+          } else if (lt < kNk) {  // one list for t and t + 1
+            sDist[st * kRows + lt] = di - 1.f;
+            sDist[st * kRows + kNk + lt] = di;
+          }
+        }
         if (shared) {  // loader warps 0 and 1 hold keys 32 w .. + 31 of the shared list
           const int u = it * kNk + lt;
           const bool win = u < ksh.n_w;
@@ -340,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         named_sync(3, kLoaders);
         if (lt == 0) mbar_arrive(&kfull[st]);
-        if (it + 1 < ntiles) nc = code_of(it + 1);
+        if (it + 1 < ntiles) nc = code_of(it + 1, nd);
       }
     } else if (warp == 4) {
       // ---------------------------------------------------------------- MMA issue
@@ -394,7 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- softmax (one head row per thread)
       const int slot = lane >> 4, h = warp * 16 + (lane & 15);
       const int b_mine = slot ? b1 : b0;
-      const float sl2 = p.sm_scale * kLog2e;
+      const float cap2 = RULE ? p.score_cap * kLog2e : 0.f;
+      const float sl2 = cap2 > 0.f ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
+      const float slope2 = RULE && p.slopes ? p.slopes[h] * kLog2e : 0.f;
       const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
       uint8_t* prow = sP + slot * (kPBytes / 2) + h * 128;
       const int sw = h & 7;
@@ -420,7 +450,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's 64 logits of this row (two loads, one wait); the row max in four chains
         const uint64_t vm = static_cast<uint64_t>(valid[0]) | (static_cast<uint64_t>(valid[1]) << 32);
         float mt;
-        {
+        uint32_t ruled[RULE ? kNk : 1];  // RULE: the logits after the rule, in log2 units
+        if constexpr (RULE) {
+          tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(ruled));
+          tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(ruled + 32));
+          tmem_ld_wait();
+          const float* dst = sDist + (gt % kNS) * kRows + slot * kNk;
+          if (cap2 > 0.f) {
+#pragma unroll
+            for (int j = 0; j < kNk; ++j)
+              ruled[j] = __float_as_uint(ruled_score<true>(__uint_as_float(ruled[j]), sl2, cap2, slope2, dst[j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < kNk; ++j)
+              ruled[j] = __float_as_uint(ruled_score<false>(__uint_as_float(ruled[j]), sl2, 0.f, slope2, dst[j]));
+          }
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < kNk; j += 2) {
+            if (!((vm >> j) & 1u)) ruled[j] = 0xff800000u;  // -inf
+            if (!((vm >> (j + 1)) & 1u)) ruled[j + 1] = 0xff800000u;
+            m0 = fmaxf(m0, __uint_as_float(ruled[j]));
+            m1 = fmaxf(m1, __uint_as_float(ruled[j + 1]));
+          }
+          mt = fmaxf(m0, m1);
+        } else {
           uint32_t s[kNk];
           tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
           tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
@@ -472,19 +526,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint8_t* pbuf = prow + (gt & 1u) * kPBytes;
         {  // the logits again (two loads, one wait), their exponentials, the row sum in two chains
-          uint32_t s[kNk];
-          tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
-          tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-          tmem_ld_wait();
           float l0 = 0.f, l1 = 0.f;
           uint32_t pp[kNk / 2];
+          if constexpr (RULE) {
 #pragma unroll
-          for (int j = 0; j < kNk / 2; ++j) {
-            const float e0 = (vm >> (2 * j)) & 1u ? exp2f(__uint_as_float(s[2 * j]) * sl2 - msub) : 0.f;
-            const float e1 = (vm >> (2 * j + 1)) & 1u ? exp2f(__uint_as_float(s[2 * j + 1]) * sl2 - msub) : 0.f;
-            l0 += e0;
-            l1 += e1;
-            pp[j] = pack_bf16(e0, e1);
+            for (int j = 0; j < kNk / 2; ++j) {
+              const float e0 = exp2f(__uint_as_float(ruled[2 * j]) - msub);
+              const float e1 = exp2f(__uint_as_float(ruled[2 * j + 1]) - msub);
+              l0 += e0;
+              l1 += e1;
+              pp[j] = pack_bf16(e0, e1);
+            }
+          } else {
+            uint32_t s[kNk];
+            tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < kNk / 2; ++j) {
+              const float e0 = (vm >> (2 * j)) & 1u ? exp2f(__uint_as_float(s[2 * j]) * sl2 - msub) : 0.f;
+              const float e1 = (vm >> (2 * j + 1)) & 1u ? exp2f(__uint_as_float(s[2 * j + 1]) * sl2 - msub) : 0.f;
+              l0 += e0;
+              l1 += e1;
+              pp[j] = pack_bf16(e0, e1);
+            }
           }
           l_run += l0 + l1;
           // keys 8 i .. 8 i + 7: 16-byte chunk i of the row (one 64-key atom)
@@ -586,12 +651,13 @@ cudaError_t launch_attend_pair(AttendParams& p, int n_sm, cudaStream_t st) {
   CUtensorMap tm_q;
   if (!encode_q(&tm_q, p.q, static_cast<uint64_t>(p.n_q) * kH)) return cudaErrorNotSupported;
   const size_t smem = Smem::bytes();
-  cudaError_t e = cudaFuncSetAttribute(attend_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  auto kern = has_score_rule(p) ? attend_pair_kernel<true> : attend_pair_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int items = (p.n_q + 1) / 2;
   const int grid = items < n_sm ? items : n_sm;
-  return launch_pdl(attend_pair_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, st, tm_q, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, st, tm_q, p);
 }
 
 }  // namespace cskv

@@ -44,8 +44,13 @@
 // keys), which makes a window tile 64 consecutive ring rows. Each item writes
 // its normalised partial output and log-sum-exp; attend_merge_t_kernel combines
 // the splits.
+//
+// RULE is the form with a cap or a distance bias on the logits: the loaders write
+// each key's distance beside its source row, and the softmax applies the rule to
+// the fp32 logits before the running max.
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
+#include "score_rule.cuh"
 
 namespace cskv {
 namespace {
@@ -71,13 +76,18 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;       // log2 units
 constexpr int kMaxSplitKeys = 1024;             // keys of one HCA work item at most (16 tiles)
 
+template <bool FP8, bool RULE>
 struct Smem {
+  // FP8 entries with a rule have both a scale and a distance per key; the tiles' source-row codes, which only the
+  // loaders read, then keep one buffer (every read of it is done when the loaders meet for the next tile)
+  static constexpr int kCodes = FP8 && RULE ? 1 : kNS;
   static constexpr int Q = 0;                          // 9 blocks of 64 heads x 128 B
   static constexpr int K = Q + kStageBytes;            // kNS key tiles
   static constexpr int P = K + kNS * kStageBytes;      // P of the tile (64 rows x 128 B)
-  static constexpr int CODE = P + kPBytes;             // [kNS][kNk] source-row codes of a stage's keys
-  static constexpr int SCALE = CODE + kNS * kNk * 4;   // [kNS][kNk] FP8 scale of each key (1 for bf16 rows)
-  static constexpr int MASK = SCALE + kNS * kNk * 4;   // [kNS][2] valid-key bits
+  static constexpr int CODE = P + kPBytes;             // [kCodes][kNk] source-row codes of a stage's keys
+  static constexpr int SCALE = CODE + kCodes * kNk * 4;  // [kNS][kNk] FP8 scale of each key (1 for bf16 rows)
+  static constexpr int DIST = SCALE + (FP8 ? kNS * kNk * 4 : 0);  // RULE: [kNS][kNk] distance of each key
+  static constexpr int MASK = DIST + (RULE || !FP8 ? kNS * kNk * 4 : 0);  // [kNS][2] valid-key bits
   static constexpr int BAR = MASK + 32;                // mbarriers
   static constexpr int TMEM = BAR + 16 * 8;            // allocated tensor-memory address
   static constexpr int FLAGS = TMEM + 16;
@@ -118,10 +128,17 @@ __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
 // Code of the source row of key u: window keys first, in ring-slot order (slot
 // u) when every window row is in the ring, in position order when a prefill
 // chunk supplies some of them; then the compressed entries. 0 if invalid.
-__device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int seq, const Keys& k, int64_t u) {
+// dist: the key's distance from the query in tokens (RULE).
+__device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int seq, const Keys& k, int64_t u,
+                                             float& dist) {
+  dist = 0.f;
   if (u < k.n_w) {
-    if (!p.x_chunk) return (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + u);
+    if (!p.x_chunk) {
+      dist = static_cast<float>((k.t - u) % p.n_win);  // slot u holds the latest position up to t that is u mod n_win
+      return (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + u);
+    }
     const int64_t pos = k.ws + u;
+    dist = static_cast<float>(k.t - pos);
     const int64_t cr = chunk_row(p, seq, pos);
     if (cr >= 0) return (3u << kRowBits) | static_cast<uint32_t>(cr);
     return (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + pos % p.n_win);
@@ -129,6 +146,7 @@ __device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int s
   const int64_t jj = u - k.n_w;
   const int64_t j = p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k + jj]) : jj;
   if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return 0;
+  dist = entry_distance(k.t, j, p.m);
   const int64_t pi = j / p.page_size;
   if (pi >= p.max_pages_per_seq) return 0;
   const int32_t page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
@@ -197,20 +215,22 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint32_t q, uint32_t k, uint
 //             store P -> named barrier -> thread 0: O += P V(gt) -> commit kempty, obar
 // FP8: the pool holds E4M3 entries with an fp32 scale each (a separate
 // instantiation keeps the bf16 kernel's code small)
-template <bool FP8>
+template <bool FP8, bool RULE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ring,
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvg,
                      AttendParams p) {
+  using Sm = Smem<FP8, RULE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = sm + Smem::Q;
-  uint8_t* sK = sm + Smem::K;
-  uint8_t* sP = sm + Smem::P;
-  uint32_t* sCode = reinterpret_cast<uint32_t*>(sm + Smem::CODE);
-  float* sScale = reinterpret_cast<float*>(sm + Smem::SCALE);
-  uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Smem::BAR);
+  uint8_t* sQ = sm + Sm::Q;
+  uint8_t* sK = sm + Sm::K;
+  uint8_t* sP = sm + Sm::P;
+  uint32_t* sCodes = reinterpret_cast<uint32_t*>(sm + Sm::CODE);
+  float* sScale = reinterpret_cast<float*>(sm + Sm::SCALE);
+  float* sDist = reinterpret_cast<float*>(sm + Sm::DIST);
+  uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Sm::MASK);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sm::BAR);
   uint64_t* kfull = bars;             // [2] loaders -> S warp (and the softmax, for the stage's key bits)
   uint64_t* kempty = bars + 2;        // [2] P V of the stage's tile done (commit)
   uint64_t* sfull = bars + 4;         // [2] S of the buffer's tile done (commit)
@@ -219,11 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* qbar = bars + 9;          //     Q of the item landed (TMA)
   uint64_t* dbar = bars + 10;         //     the item's last P V done (commit)
   constexpr bool fp8 = FP8;
-  uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
-  volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
-  volatile int* sLdOk = reinterpret_cast<int*>(sm + Smem::FLAGS) + 1;
-  volatile int* sPool = reinterpret_cast<int*>(sm + Smem::FLAGS) + 2;  // [2] per code warp: the tile is gatherable
-  int* sPref = reinterpret_cast<int*>(sm + Smem::PREF);
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Sm::TMEM);
+  volatile int* sAbort = reinterpret_cast<int*>(sm + Sm::FLAGS);
+  volatile int* sLdOk = reinterpret_cast<int*>(sm + Sm::FLAGS) + 1;
+  volatile int* sPool = reinterpret_cast<int*>(sm + Sm::FLAGS) + 2;  // [2] per code warp: the tile is gatherable
+  int* sPref = reinterpret_cast<int*>(sm + Sm::PREF);
   __shared__ int s_wsum[32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -335,11 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return -1;
       };
       // the source row of key lt of tile it (threads 0 .. kNk - 1), and its FP8 scale
-      auto code_of = [&](int it, float& sc) -> uint32_t {
+      auto code_of = [&](int it, float& sc, float& di) -> uint32_t {
         sc = 0.f;
+        di = 0.f;
         const int i = it * kNk + lt;
         if (lt >= kNk || i >= nk || !seq_ok) return 0u;
-        const uint32_t c = key_code(p, b, seq, kk, u0 + i);
+        const uint32_t c = key_code(p, b, seq, kk, u0 + i, di);
         if (!c) {
           if (grp == 0) report(p.status, CSKV_ERR_OUT_OF_RANGE);
           return 0u;
@@ -355,16 +376,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           prefetch_l2(code_row(p, c), kDqk * 2);
       };
       // the next tile's source (its page-table lookup included) is found before its stage frees
-      float nsc = 0.f;
-      uint32_t ncode = ntiles > 0 ? code_of(0, nsc) : 0u;
+      float nsc = 0.f, ndist = 0.f;
+      uint32_t ncode = ntiles > 0 ? code_of(0, nsc, ndist) : 0u;
       int nrow0 = 0;
       int nmode = ntiles > 0 ? tile_src(0, nrow0) : -1;
       if (ntiles > 0 && nmode < 0) prefetch(ncode);
       for (int it = 0; it < ntiles; ++it) {
         const uint32_t gt = g + it;
         const int st = gt & 1;
+        uint32_t* sCode = sCodes + (Sm::kCodes == 1 ? 0 : st * kNk);
         const uint32_t code = ncode;
-        const float scale = nsc;
+        const float scale = nsc, dist = ndist;
         // the first loader warp takes the stage wait (all lanes; lane 0 records the result)
         if (lw == 0) {
           bool okw = __shfl_sync(kFull, *sAbort, 0) == 0;
@@ -377,8 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lt < kNk) {
-          sCode[st * kNk + lt] = code;
-          sScale[st * kNk + lt] = code ? scale : 0.f;  // finite for every key of the tile
+          sCode[lt] = code;
+          if (FP8) sScale[st * kNk + lt] = code ? scale : 0.f;  // finite for every key of the tile
+          if (RULE) sDist[st * kNk + lt] = dist;
         }
         if (lw < 2) {
           const unsigned bits = __ballot_sync(kFull, code != 0u);
@@ -400,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < kNb; ++j) tma_load_2d(dst + j * kBlkBytes, map, j * 64, row0, &kfull[st]);
           }
           if (it + 1 < ntiles) {
-            ncode = code_of(it + 1, nsc);
+            ncode = code_of(it + 1, nsc, ndist);
             nmode = tile_src(it + 1, nrow0);
             if (nmode < 0) prefetch(ncode);
           }
@@ -414,13 +437,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             int y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t cd = sCode[st * kNk + r4 + e];
+              const uint32_t cd = sCode[r4 + e];
               y[e] = (cd >> kRowBits) == 1u ? static_cast<int>(cd & kRowMask) : -1;
             }
             tma_gather4(dst + j * kBlkBytes + r4 * 128, &tm_kvg, j * 64, y[0], y[1], y[2], y[3], &kfull[st]);
           }
           if (it + 1 < ntiles) {
-            ncode = code_of(it + 1, nsc);
+            ncode = code_of(it + 1, nsc, ndist);
             nmode = tile_src(it + 1, nrow0);
             if (nmode < 0) prefetch(ncode);
           }
@@ -438,21 +461,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint8_t* pool = static_cast<const uint8_t*>(p.kv_pool);
           for (int q = lt; q < kNk * kNb * 4; q += kLoaders) {  // (key, block, 16-byte piece)
             const int kr = q / (kNb * 4), j = (q / 4) % kNb, c4 = q % 4;
-            const uint32_t cd = sCode[st * kNk + kr];
+            const uint32_t cd = sCode[kr];
             if (cd)
               cp_async16(stg + j * kCodeBlk + kr * 64 + c4 * 16,
                          pool + (size_t)(cd & kRowMask) * kDqk + j * 64 + c4 * 16, 16);
           }
           cp_async_commit();
           if (it + 1 < ntiles) {  // the next tile's rows are looked up while the codes fly
-            ncode = code_of(it + 1, nsc);
+            ncode = code_of(it + 1, nsc, ndist);
             nmode = tile_src(it + 1, nrow0);
             if (nmode < 0) prefetch(ncode);
           }
           cp_async_wait<0>();
           // the 8 codes of bf16 chunk (key kr, block j, piece pc), and their widened store
           auto codes_at = [&](int kr, int j, int pc) -> uint2 {
-            return sCode[st * kNk + kr] ? *reinterpret_cast<const uint2*>(stg + j * kCodeBlk + kr * 64 + pc * 8)
+            return sCode[kr] ? *reinterpret_cast<const uint2*>(stg + j * kCodeBlk + kr * 64 + pc * 8)
                                         : make_uint2(0u, 0u);
           };
           auto put = [&](int kr, int j, int pc, uint2 c8) {
@@ -501,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               codes8[q] = make_uint2(0u, 0u);
               if (id < kChunks) {
                 const int kr = id / (kNb * 8), c = id % (kNb * 8);
-                const uint32_t cd = sCode[st * kNk + kr];
+                const uint32_t cd = sCode[kr];
                 if (fp8 && (cd >> kRowBits) == 1u) {
                   codes8[q] = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.kv_pool) +
                                                                    (size_t)(cd & kRowMask) * kDqk + c * 8));
@@ -519,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int id = lt + (half * (kPer / 2) + q) * kLoaders;
                 if (id < kChunks) {
                   const int kr = id / (kNb * 8), c = id % (kNb * 8);
-                  if ((sCode[st * kNk + kr] >> kRowBits) == 1u)
+                  if ((sCode[kr] >> kRowBits) == 1u)
                     *reinterpret_cast<uint4*>(dst + (c >> 3) * kBlkBytes + kr * 128 + (((c & 7) ^ (kr & 7)) << 4)) =
                         e4m3x8_to_bf16x8(codes8[q]);
                 }
@@ -528,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           cp_async_commit();
           if (it + 1 < ntiles) {  // the next tile's rows are looked up while this tile's copies fly
-            ncode = code_of(it + 1, nsc);
+            ncode = code_of(it + 1, nsc, ndist);
             nmode = tile_src(it + 1, nrow0);
             if (nmode < 0) prefetch(ncode);
           }
@@ -565,11 +588,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
       // ------------------------------------------------------------ softmax
       // thread (warp, lane): head row hr = 16 warp + (lane & 15), keys 32 kh .. + 31 of each tile
-      const float sl2 = p.sm_scale * kLog2e;
+      const float cap2 = RULE ? p.score_cap * kLog2e : 0.f;
+      const float sl2 = cap2 > 0.f ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
       const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
       const int hr = warp * 16 + (lane & 15), kh = lane >> 4;
       const uint32_t idesc_pv = umma_idesc_bf16(kH, 256, true);
       const uint32_t sKa = smem_u32(sK), sPa = smem_u32(sP);
+      const float slope2 = RULE && p.slopes ? p.slopes[grp * kH + hr] * kLog2e : 0.f;
       uint8_t* prow = sP + hr * 128;
       float m_used = -INFINITY, l_run = 0.f;
       bool ok = true;
@@ -605,17 +630,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (good) {
           const uint32_t vm = sMask[k * 2 + kh];
           const float* scl = sScale + k * kNk + 32 * kh;
+          const float* dst = sDist + k * kNk + 32 * kh;
           if (fp8) {  // an FP8 entry's logit and value carry its scale
 #pragma unroll
             for (int j = 0; j < 32; ++j) s[j] *= scl[j];
           }
+          if (RULE && cap2 > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = ruled_score<true>(s[j], sl2, cap2, slope2, dst[j]);
+          } else if (RULE) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[j] = ruled_score<false>(s[j], sl2, 0.f, slope2, dst[j]);
+          }
+          const float post = RULE ? 1.f : sl2;  // the rule has scaled its logits
           float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            s[j] = ((vm >> j) & 1u) ? s[j] * sl2 : -INFINITY;  // keys past nk have no row
-            s[j + 1] = ((vm >> (j + 1)) & 1u) ? s[j + 1] * sl2 : -INFINITY;
-            s[j + 2] = ((vm >> (j + 2)) & 1u) ? s[j + 2] * sl2 : -INFINITY;
-            s[j + 3] = ((vm >> (j + 3)) & 1u) ? s[j + 3] * sl2 : -INFINITY;
+            s[j] = ((vm >> j) & 1u) ? s[j] * post : -INFINITY;  // keys past nk have no row
+            s[j + 1] = ((vm >> (j + 1)) & 1u) ? s[j + 1] * post : -INFINITY;
+            s[j + 2] = ((vm >> (j + 2)) & 1u) ? s[j + 2] * post : -INFINITY;
+            s[j + 3] = ((vm >> (j + 3)) & 1u) ? s[j + 3] * post : -INFINITY;
             m0 = fmaxf(m0, s[j]);
             m1 = fmaxf(m1, s[j + 1]);
             m2 = fmaxf(m2, s[j + 2]);
@@ -747,9 +781,14 @@ bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box
 
 }  // namespace
 
-bool attend_tc_supported(int d_qk, int d_v, int n_heads, int kv_dtype, int n_q) {
+static size_t smem_bytes(bool fp8, bool rule, int n_q) {
+  return fp8 ? (rule ? Smem<true, true>::bytes(n_q) : Smem<true, false>::bytes(n_q))
+             : (rule ? Smem<false, true>::bytes(n_q) : Smem<false, false>::bytes(n_q));
+}
+
+bool attend_tc_supported(int d_qk, int d_v, int n_heads, int kv_dtype, int n_q, bool rule) {
   return d_qk == kDqk && d_v == kDv && n_heads % kH == 0 && (kv_dtype == CSKV_BF16 || kv_dtype == CSKV_FP8_E4M3) &&
-         Smem::bytes(n_q) + 128 <= 232448;  // the per-query prefix table shares shared memory with the tiles
+         smem_bytes(kv_dtype == CSKV_FP8_E4M3, rule, n_q) + 128 <= 232448;  // the per-query prefix table shares shared memory with the tiles
 }
 
 // keys per split: queries x head groups x splits ~ one CTA per SM
@@ -785,9 +824,10 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st) {
       !encode_rows(&tm_kvg, p.kv_dtype == CSKV_FP8_E4M3 ? static_cast<const void*>(p.ring_x) : p.kv_pool,
                    p.kv_dtype == CSKV_FP8_E4M3 ? ring_rows : kv_rows, 1))
     return cudaErrorNotSupported;
-  const size_t smem = Smem::bytes(p.n_q);
-  const bool fp8 = p.kv_dtype == CSKV_FP8_E4M3;
-  auto kern = fp8 ? attend_tc_kernel<true> : attend_tc_kernel<false>;
+  const bool fp8 = p.kv_dtype == CSKV_FP8_E4M3, rule = has_score_rule(p);
+  const size_t smem = smem_bytes(fp8, rule, p.n_q);
+  auto kern = rule ? (fp8 ? attend_tc_kernel<true, true> : attend_tc_kernel<false, true>)
+                   : (fp8 ? attend_tc_kernel<true, false> : attend_tc_kernel<false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;

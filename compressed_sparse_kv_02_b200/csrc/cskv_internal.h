@@ -162,6 +162,8 @@ struct AttendParams {
   int32_t* status;
   int rope_dims;    // inverse RoPE on the last rope_dims output channels (0: none)
   float rope_base;
+  float score_cap;      // logits capped by score_cap * tanh(. / score_cap) (0: not)
+  const float* slopes;  // [n_heads] distance bias per token, or null
   const int64_t* chunk_desc;  // [n_seqs_layer, 3] (first row, first position, length) of each sequence's chunk, or null
   // workspace / plan
   float* part_o;   // [n_q * max_splits * n_heads, d_v], or with part_t: [n_q * max_splits, d_v / 4, n_heads, 4]
@@ -172,6 +174,8 @@ struct AttendParams {
 };
 
 size_t attend_ws_bytes(const AttendParams& p, int n_sm);
+// the kernels' second form: a cap or a distance bias on the logits
+inline bool has_score_rule(const AttendParams& p) { return p.score_cap > 0.f || p.slopes; }
 
 // Row of x_chunk that holds position pos of sequence seq, or -1 (the row is then in the ring).
 // One sequence (no chunk_desc): x_chunk holds positions chunk_pos0 .. chunk_pos0 + chunk_len - 1.
@@ -196,7 +200,7 @@ cudaError_t launch_attend(AttendParams& p, void* ws, int n_sm, cudaStream_t st);
 bool attend_supported(int d_qk, int d_v, int n_heads, int kv_dtype);
 cudaError_t launch_attend_merge(AttendParams& p, cudaStream_t st);
 // tensor-core (tcgen05) attention for the 576 / 512 latent with heads in groups of 128
-bool attend_tc_supported(int d_qk, int d_v, int n_heads, int kv_dtype, int n_q);
+bool attend_tc_supported(int d_qk, int d_v, int n_heads, int kv_dtype, int n_q, bool rule);
 void attend_tc_plan(AttendParams& p, int n_sm);
 cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st);
 // tensor-core attention for calls with many queries on the 128-wide latent with 64 heads:

@@ -451,6 +451,15 @@ cskv_status csa_index_score_topk_static(const cskv_index_args* args, void* strea
  *     chunk_len is then the number of rows of x_chunk and chunk_pos0 is not
  *     used. Window rows outside a sequence's chunk come from its ring. A
  *     descriptor outside x_chunk is reported (CSKV_ERR_OUT_OF_RANGE).
+ *   score_cap, slopes: a rule on the logits, for models trained with capped
+ *     scores or with a distance bias instead of rotary positions:
+ *       s(h, u) = cap tanh(sm_scale q.k / cap) - slopes[h] (t - p_u)
+ *     score_cap = 0: no cap, else 2^-100 .. 2^100 (CSKV_ERR_INVALID_ARG outside,
+ *     where the fp32 arithmetic would overflow); slopes [n_heads] fp32 or NULL: no bias (any sign,
+ *     finite). p_u is a window token's position, and the mean position
+ *     j m + (m - 1) / 2 of the tokens of entry j's own block: a bias that is
+ *     linear in the position averages to its value there. lse is that of s.
+ *     A caller whose struct_size ends before these fields gets neither.
  * Workspace: cskv_attend_ws_bytes().
  */
 typedef struct {
@@ -475,6 +484,8 @@ typedef struct {
   int32_t rope_dims;
   float rope_base;
   const int64_t* chunk_desc;
+  float score_cap;
+  const float* slopes;
 } cskv_attend_args;
 
 cskv_status cskv_attend_ws_bytes(const cskv_attend_args* args, size_t* bytes);
