@@ -207,6 +207,9 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st);
 // query pairs, whole key lists, bf16 output written directly
 bool attend_pair_supported(const AttendParams& p, int n_sm);
 cudaError_t launch_attend_pair(AttendParams& p, int n_sm, cudaStream_t st);
+// HCA attention of a chunk with a score rule, key tiles shared by the (query, head) rows of several queries
+bool attend_chunk_supported(const AttendParams& p, int n_sm);
+cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st);
 
 // the bounded-wait check (selftest.cu)
 cudaError_t launch_wait_selftest(int arrive, uint32_t spin_limit, int32_t* status, cudaStream_t st);

@@ -10,14 +10,25 @@ namespace cskv {
 // reweighted by the error), clamped there (1 - tanh(8) = 2.3e-7). The relative form keeps small arguments, so a
 // large cap leaves the logits as they are; 1 - 2 / (1 + e^2u) would lose cap * 2^-23 and take a second
 // special-function operation, which is what bounds the capped softmax (16 per clock and SM).
+__device__ constexpr float tanh_n(int i) {  // coefficients of N and D, constant term first
+  return i == 0 ? 0.9999998807907104f : i == 1 ? 0.12925660610198975f : i == 2 ? 0.002951021073386073f
+                                                                               : 1.1428394827817101e-05f;
+}
+__device__ constexpr float tanh_d(int i) {
+  return i == 0 ? 1.f : i == 1 ? 0.46258875727653503f : i == 2 ? 0.023815542459487915f
+                      : i == 3 ? 0.00023866878473199904f : 2.4592020508862333e-07f;
+}
+// u limited to |u| <= 8; a NaN stays one
+__device__ __forceinline__ float tanh_clamp(float u) {
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, 0f41000000;\n" : "=f"(r) : "f"(u));
+  return r;
+}
 __device__ __forceinline__ float tanh_rational(float u) {
-  asm("max.NaN.f32 %0, %0, 0fC1000000;\n" : "+f"(u));  // -8; a NaN stays one
-  asm("min.NaN.f32 %0, %0, 0f41000000;\n" : "+f"(u));
+  u = tanh_clamp(u);
   const float x = u * u;
-  const float n = fmaf(fmaf(fmaf(1.1428394827817101e-05f, x, 0.002951021073386073f), x, 0.12925660610198975f), x,
-                       0.9999998807907104f);
-  const float d = fmaf(fmaf(fmaf(fmaf(2.4592020508862333e-07f, x, 0.00023866878473199904f), x, 0.023815542459487915f), x,
-                            0.46258875727653503f), x, 1.f);
+  const float n = fmaf(fmaf(fmaf(tanh_n(3), x, tanh_n(2)), x, tanh_n(1)), x, tanh_n(0));
+  const float d = fmaf(fmaf(fmaf(fmaf(tanh_d(4), x, tanh_d(3)), x, tanh_d(2)), x, tanh_d(1)), x, tanh_d(0));
   return __fdividef(u * n, d);  // d in [1, 2^7.3]
 }
 // The rule on one logit in log2 units: cap2 * tanh(s * pre) or s * pre, minus slope2 per token of distance, with

@@ -297,6 +297,31 @@ def test_masked_keys_keep_out(ck):
         s.check(bad, None, 20.0, s.slopes, sorted({0, n_q // 2, n_q - 1}))
 
 
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_chunk_nan_stays_with_the_queries_that_see_it(ck, value):
+    """A bad token and a bad entry in the middle of a chunk: queries that do not see them answer as before, those that
+    do give NaN (their softmax has a NaN logit, or a NaN or infinite value with a weight)."""
+    n, pos0, H = 1300, 1000, 64
+    chunk = {0: (0, pos0, n // 2), 1: (n // 2, 70, n // 2)}
+    seqs = [0] * (n // 2) + [1] * (n // 2)
+    pos = list(range(pos0, pos0 + n // 2)) + list(range(70, 70 + n // 2))
+    s = Setup(ck, "hca", 128, 128, H, seqs, pos, seed=17, chunk=chunk)
+    good, lse = s.run(30.0, s.slopes)
+    token, entry = pos0 + 301, 9  # entry 9 of sequence 0: visible from t = 9 * 128 + 127 on
+    s.x_chunk[token - pos0, 5] = value
+    s.L.kv_pool[s.L.rows_of(0, entry, 1), 7] = value
+    bad, bad_lse = s.run(30.0, s.slopes)
+    t = s.q_pos
+    sees = (s.q_seq == 0) & (((t >= token) & (t < token + N_WIN)) | (entry * 128 < t + 1 - N_WIN))
+    clean = ~sees
+    # the clean rows: the same keys, at most another order of the same sums (a row taken again on its own)
+    diff = (bad[clean].float() - good[clean].float()).abs()
+    assert bool((diff <= 2.0 ** -7 * (good[clean].float().abs() + 2.0)).all())
+    assert bool(((bad_lse[clean] - lse[clean]).abs() <= 1e-3).all())
+    assert not bool(torch.isfinite(bad[sees].float()).all(-1).any())
+    s.check(bad, bad_lse, 30.0, s.slopes, [i for i in range(0, n, 53) if not bool(sees[i])])
+
+
 def test_rows_without_keys(ck):
     """A position past the caller's bound or a sequence outside the layer: zeros, -inf, and the report."""
     for d_qk, d_v, H, n_q in ((128, 128, 32, 3), (576, 512, 64, 3), (128, 128, 64, 640)):
