@@ -13,22 +13,29 @@
 // with P written as bf16 over S in tensor memory (the A operand of P V) and V read
 // MN-major from the key tile. The two tiles alternate on the tensor cores: while
 // one's softmax runs, the other's P V and next S do.
-//   warps 0-3, 4-7: softmax of tile 0 / 1, one row per thread (all 128 logits of a
-//     tile in registers: the rule is applied once, then the row max, then the
-//     exponentials; O is rescaled only when the max rises by more than 2^8);
-//   warp 8: issues the MMAs;  warps 9-11: look up the keys' rows and copy them
-//     (cp.async) into four 128-byte-swizzled stages; Q by TMA.
+//   warps 0-3, 4-7: softmax of tile 0 / 1, one row per thread; O is rescaled only
+//     when the row max rises by more than 2^8. O goes out through shared memory
+//     and TMA (written by the threads, 32 rows per instruction, it took 8,700
+//     cycles per item);
+//   warp 8: issues the MMAs;
+//   warps 9, 10: look up the keys' rows, four keys per lane, and have TMA copy the
+//     two 64-channel halves of each tile: 16 consecutive rows per copy where a run
+//     of 16 keys has them, else gathers of four rows. A copy costs its warp ~150
+//     cycles whatever its size: 64 gathers by one warp took 10,000 cycles per tile,
+//     and 96 threads copying by cp.async 5,700.
 //
 // Bound: the softmax's arithmetic, not the tensor cores. A pair of 128 x 128 tiles
-// is 4 x 512 cycles of MMA and 32,768 logits. With the cap a logit takes 1.5
-// special-function operations (its exponential and half a reciprocal: two tanh share
-// one) and about 12.5 issue slots (packed f32x2 arithmetic), 3072 and 3200 cycles a
-// pair; without it 1 and 4.5, 2048 and 1150.
+// is 4 x 512 cycles of MMA and 32,768 logits. With the cap a logit takes 15 fp32
+// operations (128 per clock and SM; packed pairs halve the issue slots, not the
+// pipe time) and 1.5 special-function operations (16 per clock: its exponential and
+// half a reciprocal, which two tanh share): 3840 and 3072 cycles a pair; without it
+// 3 and 1, 770 and 2048.
 //
 // A row's segment is the run of consecutive queries of one sequence it stands in
 // (positions at most kMaxStep apart, so that a segment's windows overlap): the key
-// list of a segment is its queries' window positions wlo .. thi, then the entries
-// visible at thi, and each row's mask keeps its own window and entries. Rows that
+// list of a segment is its queries' window positions wlo .. thi, padded to a
+// multiple of four, then the entries visible at thi, and each row's mask keeps its
+// own window and entries. Rows that
 // belong to another segment of the item are masked out of the whole segment.
 //
 // Masked keys are multiplied by P = 0, which a NaN or an infinity in a masked key's
@@ -46,12 +53,10 @@ constexpr int kD = 128;                      // d_qk = d_v
 constexpr int kTileRows = 128;               // rows of one M tile
 constexpr int kItemRows = 2 * kTileRows;
 constexpr int kNk = 128;                     // keys per tile
-constexpr int kNS = 4;                       // key stages
+constexpr int kNS = 3;                       // key stages
 constexpr int kHalfBytes = kNk * 128;        // 16384: one 64-channel half of 128 rows
 constexpr int kStageBytes = 2 * kHalfBytes;  // 32768 (also one Q tile)
 constexpr int kThreads = 384;
-constexpr int kLoadThread0 = 288;
-constexpr int kLoaders = kThreads - kLoadThread0;  // 96
 constexpr int kMaxStep = 32;                 // largest step between positions of one segment's queries
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w (P over its first 64 columns), O at 256 + 128 w
@@ -62,9 +67,10 @@ constexpr float kRescaleThreshold = 8.0f;    // log2 units
 struct Smem {
   static constexpr int Q = 0;
   static constexpr int K = Q + 2 * kStageBytes;
-  static constexpr int POS = K + kNS * kStageBytes;   // [kNS][kNk] key positions relative to the segment's last query
-  static constexpr int ROWS = POS + kNS * kNk * 4;    // [2][kNk] source-row codes
-  static constexpr int MASK = ROWS + 2 * kNk * 4;     // [kNS][4] valid-key bits
+  static constexpr int OUT = K + kNS * kStageBytes;   // 64 output channels of both tiles on their way to TMA
+  static constexpr int POS = OUT + 2 * kHalfBytes;    // [kNS][kNk] key positions relative to the segment's last query
+  static constexpr int ROWS = POS + kNS * kNk * 4;    // [2][kNk] source-row codes (a tile copied by cp.async)
+  static constexpr int MASK = ROWS + 2 * kNk * 4;         // [kNS][4] valid-key bits
   static constexpr int BAR = MASK + kNS * 16;
   static constexpr int TMEM = BAR + 24 * 8;
   static constexpr int FLAGS = TMEM + 8;
@@ -84,75 +90,88 @@ __device__ __forceinline__ const uint16_t* code_row(const AttendParams& p, uint3
   if (kind == 3) return p.x_chunk + (size_t)row * kD;
   return nullptr;
 }
-__device__ __forceinline__ uint32_t window_code(const AttendParams& p, int seq, int64_t pos) {
+__device__ __forceinline__ uint32_t window_code(const AttendParams& p, int seq, int pos) {
   const int64_t cr = chunk_row(p, seq, pos);
   if (cr >= 0) return (3u << kRowBits) | static_cast<uint32_t>(cr);
   return (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + pos % p.n_win);
 }
-__device__ __forceinline__ uint32_t entry_code(const AttendParams& p, int seq, int64_t j) {
-  const int64_t pi = j / p.page_size;
+__device__ __forceinline__ uint32_t entry_code(const AttendParams& p, int seq, int j) {
+  const int pi = j / p.page_size;
   if (pi >= p.max_pages_per_seq) return 0;
   const int32_t page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
   if (page < 0 || page >= p.n_pages) return 0;
   return (1u << kRowBits) | static_cast<uint32_t>((int64_t)page * p.page_size + j % p.page_size);
 }
+// visible_entries and window_start for positions below 2^31 and m = 2^lm
+__device__ __forceinline__ int visible32(const AttendParams& p, int t, int lm) {
+  const int lim = t + 1 - p.n_win;
+  return lim <= 0 ? 0 : static_cast<int>((static_cast<unsigned>(lim) + (1u << lm) - 1u) >> lm);
+}
+__device__ __forceinline__ int start32(const AttendParams& p, int t) { return max(t - p.n_win + 1, 0); }
 
-// The queries of an item (at most 17: 16 heads or more, rows that need not begin with a query), one per lane: position (-1: no keys) and sequence.
+// The queries of an item (at most 17: 16 heads or more, rows that need not begin with a query), one per lane:
+// position (-1: no keys) and sequence.
 struct Queries {
-  int q0, n;    // first query, queries the item touches
-  int64_t t;    // this lane's
-  int seq;
+  int q0;           // first query
+  int t, seq;       // this lane's
   unsigned starts;  // lanes where a segment begins
   unsigned runs;    // lanes that belong to one
 };
-__device__ __forceinline__ Queries load_queries(const AttendParams& p, int item, int lane) {
-  Queries r;
-  const int64_t rows = (int64_t)p.n_q * p.n_heads;
-  const int64_t a = (int64_t)item * kItemRows, b = a + kItemRows < rows ? a + kItemRows : rows;
-  r.q0 = static_cast<int>(a / p.n_heads);
-  r.n = a < rows ? static_cast<int>((b - 1) / p.n_heads) - r.q0 + 1 : 0;
-  r.t = -1;
-  r.seq = -1;
-  if (lane < r.n) {
-    r.t = p.q_pos[r.q0 + lane];
-    r.seq = p.q_seq[r.q0 + lane];
-    if (r.t > p.max_pos || r.seq < 0 || r.seq >= p.n_seqs_layer) r.t = -1;
+// this lane's query of an item, read one item ahead of its use
+struct RawQuery {
+  int64_t t;
+  int seq;
+};
+__device__ __forceinline__ RawQuery fetch_query(const AttendParams& p, int item, int lane) {
+  RawQuery r = {-1, -1};
+  const int rows = p.n_q * p.n_heads;
+  const int64_t first = (int64_t)item * kItemRows;
+  if (first < rows) {
+    const int a = static_cast<int>(first), q = a / p.n_heads + lane;
+    if (q <= (min(a + kItemRows, rows) - 1) / p.n_heads) {
+      r.t = p.q_pos[q];
+      r.seq = p.q_seq[q];
+    }
   }
-  const bool ok = r.t >= 0;
-  const int64_t tp = __shfl_up_sync(kFull, r.t, 1);
+  return r;
+}
+__device__ __forceinline__ Queries item_queries(const AttendParams& p, int item, RawQuery raw, int lane) {
+  Queries r;
+  r.q0 = item * kItemRows / p.n_heads;
+  const bool ok = raw.t >= 0 && raw.t <= p.max_pos && raw.seq >= 0 && raw.seq < p.n_seqs_layer;
+  r.t = ok ? static_cast<int>(raw.t) : -1;
+  r.seq = raw.seq;
+  const int tp = __shfl_up_sync(kFull, r.t, 1);
   const int sp = __shfl_up_sync(kFull, r.seq, 1);
-  const int64_t step = r.t - tp;
-  const bool cont = lane > 0 && tp >= 0 && sp == r.seq && step <= kMaxStep && step >= -kMaxStep;
+  const bool cont = lane > 0 && tp >= 0 && sp == r.seq && abs(r.t - tp) <= kMaxStep;
   r.starts = __ballot_sync(kFull, ok && !cont);
   r.runs = __ballot_sync(kFull, ok);
   return r;
 }
 
-// One segment: lanes s .. e - 1, its key list (n_w window positions wlo .. thi, then nv entries).
+// One segment: lanes s .. e - 1, its key list (window positions wlo .. thi in n_w places, then entries, n in all).
 struct Segment {
-  int s, e, seq, n_w, n, ntiles;
-  int64_t wlo, thi;
+  int s, e, seq, n_w, n, ntiles, wlo, thi;
 };
-__device__ __forceinline__ Segment segment_at(const AttendParams& p, const Queries& q, int s, int lane) {
+__device__ __forceinline__ Segment segment_at(const AttendParams& p, const Queries& q, int s, int lane, int lm) {
   Segment g;
   g.s = s;
   const unsigned after = ~((2u << s) - 1u);  // lanes past s
   const unsigned stop = (q.starts | ~q.runs) & after;
   g.e = stop ? __ffs(stop) - 1 : 32;
   g.seq = __shfl_sync(kFull, q.seq, s);
-  const int64_t t0 = __shfl_sync(kFull, q.t, s);
-  const int d = lane >= s && lane < g.e ? static_cast<int>(q.t - t0) : 0;  // a segment spans at most 16 kMaxStep
-  const int64_t tlo = t0 + __reduce_min_sync(kFull, d);
-  g.thi = t0 + __reduce_max_sync(kFull, d);
-  g.wlo = window_start(tlo, p.n_win);
-  g.n_w = static_cast<int>(g.thi - g.wlo + 1);
-  g.n = g.n_w + static_cast<int>(visible_entries(g.thi, p.m, p.n_win));
+  const int ts = __shfl_sync(kFull, q.t, s);
+  const int t = lane >= s && lane < g.e ? q.t : ts;
+  g.thi = __reduce_max_sync(kFull, t);
+  g.wlo = start32(p, __reduce_min_sync(kFull, t));
+  g.n_w = (g.thi - g.wlo + 4) & ~3;
+  g.n = g.n_w + visible32(p, g.thi, lm);
   g.ntiles = (g.n + kNk - 1) / kNk;
   return g;
 }
-__device__ __forceinline__ int item_tiles(const AttendParams& p, const Queries& q, int lane) {
+__device__ __forceinline__ int item_tiles(const AttendParams& p, const Queries& q, int lane, int lm) {
   int n = 0;
-  for (unsigned m = q.starts; m; m &= m - 1) n += segment_at(p, q, __ffs(m) - 1, lane).ntiles;
+  for (unsigned m = q.starts; m; m &= m - 1) n += segment_at(p, q, __ffs(m) - 1, lane, lm).ntiles;
   return n;
 }
 
@@ -162,16 +181,48 @@ __device__ __forceinline__ uint32_t range_bits(int a, int lo, int hi) {
   return h > l ? (0xffffffffu >> (32 - (h - l))) << l : 0u;
 }
 
-// named barrier over n threads that also returns the OR of `v` over them (the same in every thread)
-__device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
+// The MMAs are issued by one elected lane, but by code that the whole warp runs together: the descriptors then sit in
+// uniform registers. Inside a branch on the lane every one of them is moved there first, which held an MMA up for
+// ~140 cycles (64 is what it takes to run).
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
-  asm volatile(
-      "{\n .reg .pred q, p;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
 }
+__device__ __forceinline__ void umma_ss_if(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_if(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t issue, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
+}
+
+// 2D tiled TMA store from shared memory, and its bulk-group bookkeeping (per issuing thread)
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
 // ---------------------------------------------------------------- packed fp32 pairs
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -202,25 +253,120 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
   return r;
 }
-// cap2 tanh(s pre) + bias of two logits; the two quotients share one reciprocal of d0 d1 (each at most 2^7.3)
-__device__ __forceinline__ uint64_t capped2(uint64_t s, uint64_t pre, float cap2, uint64_t bias) {
-  uint64_t u = mul2(s, pre);
-  float u0, u1, d0, d1;
-  unpack2(u, u0, u1);
-  u0 = tanh_clamp(u0);
-  u1 = tanh_clamp(u1);
-  u = pack2(u0, u1);
-  const uint64_t x = mul2(u, u);
-  uint64_t n = pack2(tanh_n(3), tanh_n(3)), d = pack2(tanh_d(4), tanh_d(4));
-#pragma unroll
-  for (int i = 2; i >= 0; --i) n = fma2(n, x, pack2(tanh_n(i), tanh_n(i)));
-#pragma unroll
-  for (int i = 3; i >= 0; --i) d = fma2(d, x, pack2(tanh_d(i), tanh_d(i)));
-  unpack2(d, d0, d1);
+// a max of three, and of the magnitudes of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(d0 * d1));
-  r *= cap2;
-  return fma2(mul2(mul2(u, n), pack2(d1, d0)), pack2(r, r), bias);
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// cap tanh(s pre) as a polynomial in s where |s pre| <= 1, to a relative error of 6e-7: tanh(u) / u in u^2 on [0, 1]
+// (fitted like tanh_rational), its coefficients times cap2 pre^(2i + 1). Logits seldom reach the cap, so most tiles
+// take this form: 7 fp32 operations a logit instead of 12, and no reciprocal.
+__device__ constexpr float tanh_p(int i) {
+  return i == 0 ? 0.9999994039535522f : i == 1 ? -0.3332904279232025f : i == 2 ? 0.13281434774398804f
+                      : i == 3 ? -0.051605693995952606f : i == 4 ? 0.016743136569857597f : -0.0030670680571347475f;
+}
+struct Rule {
+  float pre, cap2;  // capped: sm_scale / cap and cap log2(e); else sm_scale log2(e) and 0
+  float lim;        // |s| up to here takes the polynomial (negative: never)
+  float c[6];
+};
+__device__ __forceinline__ Rule make_rule(const AttendParams& p, bool cap) {
+  Rule r;
+  r.cap2 = cap ? p.score_cap * kLog2e : 0.f;
+  r.pre = cap ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
+  r.lim = r.pre < 2048.f ? 1.f / r.pre : -1.f;  // above that pre^10 would leave fp32's range
+  float f = r.cap2 * r.pre;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    r.c[i] = f * tanh_p(i);
+    f *= r.pre * r.pre;
+  }
+  return r;
+}
+
+// The rule on 64 logits, packed pairs of four at a time in step: with the cap, without, or capped below lim. bias =
+// slope2 * position - ref, ref the row's running maximum so far (its subtraction costs nothing here). Independent
+// chains in step keep a scheduler with two softmax warps issuing (pair after pair left it idle 2/3 of the time).
+enum { kLinear, kRational, kPoly };
+template <int FORM>
+__device__ __forceinline__ void rule64(uint32_t (&s)[64], const float4* pos, const Rule& r, uint64_t slope,
+                                       uint64_t negref) {
+  const uint64_t pre = pack2(r.pre, r.pre), cap2 = pack2(r.cap2, r.cap2);
+#pragma unroll
+  for (int b = 0; b < 64; b += 8) {
+    const float4 pa = pos[b / 4], pb = pos[b / 4 + 1];
+    uint64_t u[4], bias[4] = {fma2(slope, pack2(pa.x, pa.y), negref), fma2(slope, pack2(pa.z, pa.w), negref),
+                              fma2(slope, pack2(pb.x, pb.y), negref), fma2(slope, pack2(pb.z, pb.w), negref)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = pack2(__uint_as_float(s[b + 2 * j]), __uint_as_float(s[b + 2 * j + 1]));
+    if constexpr (FORM == kLinear) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = fma2(u[j], pre, bias[j]);
+    } else if constexpr (FORM == kPoly) {
+      uint64_t x[4], n[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], u[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n[j] = fma2(pack2(r.c[5], r.c[5]), x[j], pack2(r.c[4], r.c[4]));
+#pragma unroll
+      for (int i = 3; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = fma2(n[j], x[j], pack2(r.c[i], r.c[i]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = fma2(u[j], n[j], bias[j]);
+    } else {
+      uint64_t x[4], n[4], d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], pre);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float u0, u1;
+        unpack2(u[j], u0, u1);
+        u[j] = pack2(tanh_clamp(u0), tanh_clamp(u1));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], u[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[j] = fma2(pack2(tanh_d(4), tanh_d(4)), x[j], pack2(tanh_d(3), tanh_d(3)));
+#pragma unroll
+      for (int i = 2; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = fma2(d[j], x[j], pack2(tanh_d(i), tanh_d(i)));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n[j] = fma2(pack2(tanh_n(3), tanh_n(3)), x[j], pack2(tanh_n(2), tanh_n(2)));
+#pragma unroll
+      for (int i = 1; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) n[j] = fma2(n[j], x[j], pack2(tanh_n(i), tanh_n(i)));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) n[j] = mul2(n[j], u[j]);
+      // two quotients share one reciprocal: 1 / d_a = d_b / (d_a d_b), each d at most 2^7.3
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        float q0, q1, r0, r1;
+        unpack2(mul2(d[j], d[j + 1]), q0, q1);
+        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r0) : "f"(q0));
+        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r1) : "f"(q1));
+        const uint64_t rc = mul2(pack2(r0, r1), cap2);
+        u[j] = fma2(mul2(n[j], d[j + 1]), rc, bias[j]);
+        u[j + 1] = fma2(mul2(n[j + 1], d[j]), rc, bias[j + 1]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float a, c;
+      unpack2(u[j], a, c);
+      s[b + 2 * j] = __float_as_uint(a);
+      s[b + 2 * j + 1] = __float_as_uint(c);
+    }
+  }
 }
 
 // One row from its own keys only, by one warp (lane = 4 channels): scores in fp32, an online softmax, fp32 P.
@@ -228,16 +374,16 @@ template <bool CAP>
 __device__ __noinline__ void slow_row(const AttendParams& p, int64_t row, float sl2, float cap2, float slope2, float (&o)[4],
                                       float& m, float& l, int lane) {
   const int b = static_cast<int>(row / p.n_heads);
-  const int64_t t = p.q_pos[b], ws = window_start(t, p.n_win);
+  const int t = static_cast<int>(p.q_pos[b]), ws = start32(p, t);
   const int seq = p.q_seq[b];
-  const int64_t n_w = t - ws + 1, n = n_w + visible_entries(t, p.m, p.n_win);
+  const int n_w = t - ws + 1, n = n_w + visible32(p, t, __ffs(p.m) - 1);
   const uint2 qv = *reinterpret_cast<const uint2*>(p.q + row * kD + 4 * lane);
   const __nv_bfloat162* q2 = reinterpret_cast<const __nv_bfloat162*>(&qv);
   const float2 qa = __bfloat1622float2(q2[0]), qb = __bfloat1622float2(q2[1]);
   o[0] = o[1] = o[2] = o[3] = 0.f;
   m = -INFINITY;
   l = 0.f;
-  for (int64_t u = 0; u < n; ++u) {
+  for (int u = 0; u < n; ++u) {
     const uint32_t c = u < n_w ? window_code(p, seq, ws + u) : entry_code(p, seq, u - n_w);
     const uint16_t* src = code_row(p, c);
     if (!src) continue;
@@ -260,37 +406,42 @@ __device__ __noinline__ void slow_row(const AttendParams& p, int64_t row, float 
   }
 }
 
-// Pipeline (key tiles numbered g over the CTA's items; stage g % 4):
-//   loaders : look up rows -> wait kempty (P V of tile g - 4) -> cp.async -> kfull (one tile later, once landed)
+// Pipeline (key tiles numbered g over the CTA's items; stage g % 2):
+//   loader  : look up rows -> wait kempty (P V of tile g - 2) -> TMA gathers -> kfull
 //   MMA     : S0(0) S1(0), then per key tile: wait pfull0 -> P V 0(g), S0(g + 1) -> sfull0 (or odone0);
 //             wait pfull1 -> P V 1(g) -> kempty, S1(g + 1) -> sfull1 (or odone1); the last S1 of an item -> qempty
 //   softmax : wait sfull (S here, and every earlier P V of this tile done: O may be rescaled) -> P -> pfull;
 //             after the item's last tile: wait odone -> read O -> oread, which the next item's first P V waits for
 template <bool CAP>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttendParams p) {
+    attend_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_pool,
+                        const __grid_constant__ CUtensorMap tm_ring, const __grid_constant__ CUtensorMap tm_chunk,
+                        const __grid_constant__ CUtensorMap tm_pool16, const __grid_constant__ CUtensorMap tm_ring16,
+                        const __grid_constant__ CUtensorMap tm_chunk16, const __grid_constant__ CUtensorMap tm_out,
+                        const __grid_constant__ AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Smem::Q;
   uint8_t* sK = sm + Smem::K;
+  uint8_t* sO = sm + Smem::OUT;
   float* sPos = reinterpret_cast<float*>(sm + Smem::POS);
   uint32_t* sRow = reinterpret_cast<uint32_t*>(sm + Smem::ROWS);
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
-  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + Smem::BAR);  // [4] loaders (96) -> MMA, softmax
-  uint64_t* kempty = kfull + kNS;                                 // [4] MMA -> loaders
+  uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + Smem::BAR);  // [3] loaders (2) -> MMA, softmax
+  uint64_t* kempty = kfull + kNS;                                 // [3] MMA -> loaders
   uint64_t* sfull = kempty + kNS;                                 // [2] MMA -> softmax
   uint64_t* pfull = sfull + 2;                                    // [2] softmax (4 warps) -> MMA
   uint64_t* odone = pfull + 2;                                    // [2] MMA -> softmax
   uint64_t* oread = odone + 2;                                    // [2] softmax (4 warps) -> MMA
-  uint64_t* qfull = oread + 2;                                    //     Q landed (TMA)
-  uint64_t* qempty = qfull + 1;                                   //     the item's S products are done
+  uint64_t* qfull = oread + 2;                                    // [2] Q of the tile landed (TMA)
+  uint64_t* qempty = qfull + 2;                                   // [2] the item's S products of the tile are done
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNS; ++i) {
-      mbar_init(&kfull[i], kLoaders);
+      mbar_init(&kfull[i], 2);
       mbar_init(&kempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -298,13 +449,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&pfull[i], 4);
       mbar_init(&odone[i], 1);
       mbar_init(&oread[i], 4);
+      mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], 1);
     }
-    mbar_init(qfull, 1);
-    mbar_init(qempty, 1);
     fence_barrier_init();
     *sAbort = 0;
   }
-  if (tid == kLoadThread0) prefetch_tensormap(&tm_q);
+  if (tid == 288) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_pool16);
+    prefetch_tensormap(&tm_chunk16);
+    prefetch_tensormap(&tm_out);
+  }
   if (warp == 8) {
     tmem_alloc(sTmem, kTmemCols);
     tmem_relinquish();
@@ -323,207 +479,267 @@ __global__ void __launch_bounds__(kThreads, 1)
       else if (p.q_seq[b] < 0 || p.q_seq[b] >= p.n_seqs_layer)
         report(p.status, CSKV_ERR_OUT_OF_RANGE);
     }
-  const int64_t rows = (int64_t)p.n_q * p.n_heads;
-  const int n_items = static_cast<int>((rows + kItemRows - 1) / kItemRows);
-  const float cap2 = CAP ? p.score_cap * kLog2e : 0.f;
-  const float sl2 = CAP ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
+  const int rows = p.n_q * p.n_heads;
+  const int n_items = (rows + kItemRows - 1) / kItemRows;
+  const int lm = __ffs(p.m) - 1;  // m is a power of two
   uint32_t g = 0;      // key tiles before the current item
   uint32_t n_act = 0;  // items with keys before the current one
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
     if (warp == 8) {
       // ---------------------------------------------------------------- MMA issue (lane 0; the warp waits together)
-      const bool issuer = lane == 0;
-      const uint32_t idesc_s = umma_idesc_bf16(kTileRows, kNk, false);
-      const uint32_t idesc_pv = umma_idesc_bf16(kTileRows, kD, true);
+      const uint32_t issuer = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kTileRows, kNk, false);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(kTileRows, kD, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
       auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, p.status)); };
-      auto issue_s = [&](int w, uint32_t gt) {  // S of tile w: 8 K-steps over the two 64-channel halves
-        if (issuer) {
-          const uint32_t q = sQa + w * kStageBytes, k = sKa + (gt % kNS) * kStageBytes;
+      auto s_of = [&](int w, int st) {  // S of tile w from stage st: 8 K-steps over the two 64-channel halves
+        const uint32_t q = sQa + w * kStageBytes, k = sKa + st * kStageBytes;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32u;
-            umma_ss(tmem + kColS + w * kNk, umma_desc_sw128(q + off, 16, 1024), umma_desc_sw128(k + off, 16, 1024),
-                    idesc_s, ks > 0 ? 1u : 0u);
-          }
-          umma_commit(&sfull[w]);
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32u;
+          umma_ss_if(issuer, tmem + kColS + w * kNk, umma_desc_sw128(q + off, 16, 1024), umma_desc_sw128(k + off, 16, 1024),
+                     idesc_s, ks > 0 ? 1u : 0u);
         }
-        __syncwarp();
       };
-      auto issue_pv = [&](int w, uint32_t gt, bool acc) {  // O += P V of tile w: 8 K-steps of 16 keys
-        if (issuer) {
-          const uint32_t v = sKa + (gt % kNS) * kStageBytes;
+      auto pv_of = [&](int w, int st, uint32_t acc) {  // O += P V of tile w: 8 K-steps of 16 keys
+        const uint32_t v = sKa + st * kStageBytes;
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_ts(tmem + kColO + w * kD, tmem + kColS + w * kNk + ks * 8,
-                    umma_desc_sw128(v + ks * 16 * 128, kHalfBytes, 1024), idesc_pv, (acc || ks > 0) ? 1u : 0u);
-        }
-        __syncwarp();
+        for (int ks = 0; ks < 8; ++ks)
+          umma_ts_if(issuer, tmem + kColO + w * kD, tmem + kColS + w * kNk + ks * 8,
+                     umma_desc_sw128(v + ks * 16 * 128, kHalfBytes, 1024), idesc_pv, ks > 0 ? 1u : acc);
       };
+      // the stage as a constant in each branch, so that the descriptors are
+      auto issue_s = [&](int w, uint32_t gt) {
+        const uint32_t st = gt % kNS;
+        if (st == 0) s_of(w, 0);
+        else if (st == 1) s_of(w, 1);
+        else s_of(w, 2);
+        commit_if(issuer, &sfull[w]);
+      };
+      auto issue_pv = [&](int w, uint32_t gt, bool acc) {
+        const uint32_t st = gt % kNS;
+        if (st == 0) pv_of(w, 0, acc);
+        else if (st == 1) pv_of(w, 1, acc);
+        else pv_of(w, 2, acc);
+      };
+      static_assert(kNS == 3, "the stage branches");
+      // the items with keys, found one ahead: S of the next item's first key tile is issued behind P V of this
+      // item's last one, so the softmax of a tile goes from item to item without a pause
+      int item = blockIdx.x;
+      RawQuery raw = fetch_query(p, item, lane);
+      auto next_tiles = [&]() {  // key tiles of the next item that has any, 0 at the end
+        for (; item < n_items;) {
+          const int n = item_tiles(p, item_queries(p, item, raw, lane), lane, lm);
+          item += gridDim.x;
+          raw = fetch_query(p, item, lane);
+          if (n) return n;
+        }
+        return 0;
+      };
+      int ntot = next_tiles();
       bool ok = true;
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const int ntot = item_tiles(p, load_queries(p, item, lane), lane);
-        if (ntot == 0) continue;
-        if (!(ok = wait(qfull, n_act & 1u) && wait(&kfull[g % kNS], (g / kNS) & 1u))) break;
-        tc_fence_after();
-        issue_s(0, g);
-        issue_s(1, g);
-        if (ntot == 1 && issuer) umma_commit(qempty);
+      if (ntot) {
+        for (int w = 0; w < 2 && ok; ++w) {
+          ok = wait(&qfull[w], 0) && wait(&kfull[0], 0);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(w, 0);
+          if (ntot == 1) commit_if(issuer, &qempty[w]);
+        }
+      }
+      while (ntot && ok) {
+        const int nnext = next_tiles();
         for (int it = 0; it < ntot && ok; ++it) {
           if (__shfl_sync(kFull, *sAbort, 0)) {
             ok = false;
             break;
           }
           const uint32_t gt = g + it, gn = gt + 1;
-          const bool more = it + 1 < ntot;
-          ok = wait(&pfull[0], gt & 1u) && (it > 0 || n_act == 0 || wait(&oread[0], (n_act - 1) & 1u));
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(0, gt, it > 0);
-          if (more) {
-            if (!(ok = wait(&kfull[gn % kNS], (gn / kNS) & 1u))) break;
+          const bool last = it + 1 == ntot, more = !last || nnext > 0;
+          const bool qlast = last ? nnext == 1 : it + 2 == ntot;  // the next S is the last one of its item
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            ok = wait(&pfull[w], gt & 1u) && (it > 0 || n_act == 0 || wait(&oread[w], (n_act - 1) & 1u));
+            if (!ok) break;
             tc_fence_after();
-            issue_s(0, gn);
-          } else if (issuer) {
-            umma_commit(&odone[0]);
+            issue_pv(w, gt, it > 0);
+            if (w == 1) commit_if(issuer, &kempty[gt % kNS]);
+            if (last) commit_if(issuer, &odone[w]);
+            if (more) {
+              ok = (!last || wait(&qfull[w], (n_act + 1) & 1u)) && wait(&kfull[gn % kNS], (gn / kNS) & 1u);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(w, gn);
+              if (qlast) commit_if(issuer, &qempty[w]);
+            }
+            __syncwarp();
           }
-          ok = wait(&pfull[1], gt & 1u) && (it > 0 || n_act == 0 || wait(&oread[1], (n_act - 1) & 1u));
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(1, gt, it > 0);
-          if (issuer) umma_commit(&kempty[gt % kNS]);
-          if (more) {
-            issue_s(1, gn);
-            if (it + 2 == ntot && issuer) umma_commit(qempty);
-          } else if (issuer) {
-            umma_commit(&odone[1]);
-          }
-          __syncwarp();
         }
+        if (!ok) break;
         g += ntot;
         ++n_act;
+        ntot = nnext;
       }
       if (!ok) {
         *sAbort = 1;
         // what was issued gets a bounded chance to land before the tensor memory is freed
-        if (issuer) umma_commit(&odone[0]);
+        commit_if(issuer, &odone[0]);
         __syncwarp();
         mbar_wait(&odone[0], n_act & 1u, nullptr);
       }
-    } else {
-      // ---------------------------------------------------------------- loaders
-      const int lt = tid - kLoadThread0, lw = lt >> 5;
+    } else if (warp < 11) {
+      // ---------------------------------------------------------------- loaders (a warp per channel half and Q tile)
+      const int half = warp - 9;
       bool ok = true;
+      uint32_t issued = 0, q_issued = 0;  // key tiles and Q loads given to TMA
+      RawQuery raw = fetch_query(p, blockIdx.x, lane);
       for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const Queries q = load_queries(p, item, lane);
-        const int ntot = item_tiles(p, q, lane);
+        const Queries q = item_queries(p, item, raw, lane);
+        raw = fetch_query(p, item + gridDim.x, lane);
+        const int ntot = item_tiles(p, q, lane, lm);
         if (ntot == 0) continue;
-        if (lw == 0) {  // Q once the last item's S products are done with it
-          const bool free = __all_sync(kFull, n_act == 0 || mbar_wait(qempty, (n_act - 1) & 1u, p.status));
-          if (!free) {
-            *sAbort = 1;
-          } else if (lane == 0) {
-            mbar_arrive_expect_tx(qfull, 2 * kStageBytes);
-            const int row0 = item * kItemRows;
-            for (int w = 0; w < 2; ++w)
-              for (int h = 0; h < 2; ++h)
-                tma_load_2d(sQ + w * kStageBytes + h * kHalfBytes, &tm_q, h * 64, row0 + w * kTileRows, qfull);
-          }
-          __syncwarp();
+        // Q of a tile once the last item's S products are done with it
+        ok = __all_sync(kFull, n_act == 0 || mbar_wait(&qempty[half], (n_act - 1) & 1u, p.status));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&qfull[half], kStageBytes);
+          for (int h = 0; h < 2; ++h)
+            tma_load_2d(sQ + half * kStageBytes + h * kHalfBytes, &tm_q, h * 64, item * kItemRows + half * kTileRows,
+                        &qfull[half]);
         }
+        __syncwarp();
+        ++q_issued;
         uint32_t gt = g;
         for (unsigned ms = q.starts; ms && ok; ms &= ms - 1) {
-          const Segment sg = segment_at(p, q, __ffs(ms) - 1, lane);
+          const Segment sg = segment_at(p, q, __ffs(ms) - 1, lane, lm);
           for (int it = 0; it < sg.ntiles; ++it, ++gt) {
             const int st = gt % kNS;
-            // keys lt and (threads 0-31) 96 + lt of the tile: source row and position
-            uint32_t code[2] = {0u, 0u};
-            float pos[2] = {0.f, 0.f};
+            // keys u .. u + 3 of the list: all window places, or all entries (of one page)
+            const int u = it * kNk + 4 * lane;
+            uint32_t code[4] = {0u, 0u, 0u, 0u};
+            float pos[4];
+            if (u < sg.n_w) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int u = it * kNk + h * kLoaders + lt;
-              if ((h == 0 || lw == 0) && u < sg.n) {
-                if (u < sg.n_w) {
-                  code[h] = window_code(p, sg.seq, sg.wlo + u);
-                  pos[h] = static_cast<float>(sg.wlo + u - sg.thi);
-                } else {
-                  code[h] = entry_code(p, sg.seq, u - sg.n_w);
-                  pos[h] = -entry_distance(sg.thi, u - sg.n_w, p.m);
-                }
-                if (!code[h]) report(p.status, CSKV_ERR_OUT_OF_RANGE);
+              for (int e = 0; e < 4; ++e) {
+                const int at = sg.wlo + u + e;
+                if (at <= sg.thi) code[e] = window_code(p, sg.seq, at);
+                pos[e] = static_cast<float>(at - sg.thi);
+              }
+            } else {
+              const int j = u - sg.n_w, left = sg.n - u;
+              const uint32_t c = left > 0 ? entry_code(p, sg.seq, j) : 0u;
+              if (half == 0 && left > 0 && !c) report(p.status, CSKV_ERR_OUT_OF_RANGE);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (c && e < left) code[e] = c + e;
+                pos[e] = -entry_distance(sg.thi, j + e, p.m);
               }
             }
-            const bool free = gt < kNS || mbar_wait(&kempty[st], ((gt / kNS) - 1) & 1u, p.status);
-            uint32_t* row = sRow + (gt & 1) * kNk;
-            row[lt] = code[0];
-            sPos[st * kNk + lt] = pos[0];
-            const unsigned b0 = __ballot_sync(kFull, code[0] != 0u), b1 = __ballot_sync(kFull, code[1] != 0u);
-            if (lw == 0) {
-              row[kLoaders + lt] = code[1];
-              sPos[st * kNk + kLoaders + lt] = pos[1];
+            // one source per group, so that TMA can gather it (a group that straddles the ring and the chunk cannot)
+            const uint32_t kind = max(max(code[0], code[1]), max(code[2], code[3])) >> kRowBits;
+            bool one = true;
+            uint32_t bits = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              one = one && (code[e] == 0u || (code[e] >> kRowBits) == kind);
+              bits |= (code[e] ? 1u : 0u) << (4 * (lane & 7) + e);
             }
-            if (lane == 0) {
-              sMask[st * 4 + lw] = b0;
-              if (lw == 0) sMask[st * 4 + 3] = b1;
+            const bool gather = __all_sync(kFull, one);
+            // runs of 16 keys (4 lanes) in 16 consecutive rows of one source
+            const uint32_t c0 = __shfl_sync(kFull, code[0], lane & ~3);
+            bool run = code[0] != 0u && code[0] == c0 + 4 * (lane & 3);
+#pragma unroll
+            for (int e = 1; e < 4; ++e) run = run && code[e] == code[0] + e;
+            run = ((__ballot_sync(kFull, run) >> (lane & ~3)) & 15u) == 15u;
+            bits |= __shfl_xor_sync(kFull, bits, 1);
+            bits |= __shfl_xor_sync(kFull, bits, 2);
+            bits |= __shfl_xor_sync(kFull, bits, 4);
+            ok = __all_sync(kFull, gt < kNS || mbar_wait(&kempty[st], ((gt / kNS) - 1) & 1u, p.status)) &&
+                 !__any_sync(kFull, *sAbort != 0);
+            if (!ok) break;
+            if (half == 0) {
+              reinterpret_cast<float4*>(sPos + st * kNk)[lane] = make_float4(pos[0], pos[1], pos[2], pos[3]);
+              if ((lane & 7) == 0) sMask[st * 4 + (lane >> 3)] = bits;
             }
-            if (named_sync_or(3, kLoaders, !free || *sAbort)) {
-              *sAbort = 1;
-              ok = false;
-              break;
-            }
-            uint8_t* dst = sK + st * kStageBytes;
+            uint8_t* dst = sK + st * kStageBytes + half * kHalfBytes;
+            __syncwarp();
+            if (gather) {
+              if (lane == 0) mbar_arrive_expect_tx(&kfull[st], kHalfBytes);
+              __syncwarp();
+              if (run) {
+                const CUtensorMap* map = kind == 3u ? &tm_chunk16 : kind == 2u ? &tm_ring16 : &tm_pool16;
+                if ((lane & 3) == 0)
+                  tma_load_2d(dst + lane * 512, map, half * 64, static_cast<int>(code[0] & kRowMask), &kfull[st]);
+              } else {
+                const CUtensorMap* map = kind == 3u ? &tm_chunk : kind == 2u ? &tm_ring : &tm_pool;
+                int y[4];  // a key without a row reads row -1, outside the map: zeros
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = code[e] ? static_cast<int>(code[e] & kRowMask) : -1;
+                tma_gather4(dst + lane * 512, map, half * 64, y[0], y[1], y[2], y[3], &kfull[st]);
+              }
+              __syncwarp();
+            } else {
+              reinterpret_cast<uint4*>(sRow + half * kNk)[lane] = make_uint4(code[0], code[1], code[2], code[3]);
+              __syncwarp();
 #pragma unroll 4
-            for (int id = lt; id < kNk * 16; id += kLoaders) {  // 16 consecutive threads copy one 256-byte row
-              const int key = id >> 4, c = id & 15;
-              const uint16_t* src = code_row(p, row[key]);
-              cp_async16(dst + (c >> 3) * kHalfBytes + key * 128 + (((c & 7) ^ (key & 7)) << 4),
-                         src ? static_cast<const void*>(src + c * 8) : static_cast<const void*>(p.q), src ? 16 : 0);
-            }
-            cp_async_commit();
-            if (gt > g) {  // the tile before this one has landed
-              cp_async_wait<1>();
+              for (int id = lane; id < kNk * 8; id += 32) {  // 8 consecutive lanes copy half a row
+                const int key = id >> 3, c = id & 7;
+                const uint16_t* src = code_row(p, sRow[half * kNk + key]);
+                cp_async16(dst + key * 128 + ((c ^ (key & 7)) << 4),
+                           src ? static_cast<const void*>(src + half * 64 + c * 8) : static_cast<const void*>(p.q),
+                           src ? 16 : 0);
+              }
+              cp_async_commit();
+              cp_async_wait<0>();
               fence_proxy_async_smem();
-              mbar_arrive(&kfull[(gt - 1) % kNS]);
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&kfull[st]);
             }
+            issued = gt + 1;
           }
         }
-        cp_async_wait<0>();
-        if (!ok) break;
-        fence_proxy_async_smem();
-        mbar_arrive(&kfull[(gt - 1) % kNS]);
         g += ntot;
         ++n_act;
+      }
+      if (!ok) {  // the copies in flight get a bounded chance to land before the block leaves
+        *sAbort = 1;
+        for (uint32_t i = issued > kNS ? issued - kNS : 0; i < issued; ++i)
+          mbar_wait(&kfull[i % kNS], (i / kNS) & 1u, nullptr);
+        if (q_issued > 0) mbar_wait(&qfull[half], (q_issued - 1) & 1u, nullptr);
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax (one row per thread)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
     const int w = warp >> 2;
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t sb = trow + kColS + w * kNk, ob = trow + kColO + w * kD;
+    const Rule r = make_rule(p, CAP);
     bool ok = true;
+    RawQuery raw = fetch_query(p, blockIdx.x, lane);
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const Queries q = load_queries(p, item, lane);
-      const int64_t row = (int64_t)item * kItemRows + w * kTileRows + (warp & 3) * 32 + lane;
+      const Queries q = item_queries(p, item, raw, lane);
+      raw = fetch_query(p, item + gridDim.x, lane);
+      const int row = item * kItemRows + w * kTileRows + (warp & 3) * 32 + lane;
       const bool in = row < rows;
-      const int qi = in ? static_cast<int>(row / p.n_heads) - q.q0 : 0;  // this row's query lane
-      const int h = in ? static_cast<int>(row % p.n_heads) : 0;
-      const int64_t t = __shfl_sync(kFull, q.t, qi);
+      const int qi = in ? row / p.n_heads - q.q0 : 0;  // this row's query lane
+      const int h = in ? row % p.n_heads : 0;
+      const int t = __shfl_sync(kFull, q.t, qi);
       const float slope2 = p.slopes ? p.slopes[h] * kLog2e : 0.f;
-      const int ntot = item_tiles(p, q, lane);
+      const int ntot = item_tiles(p, q, lane, lm);
       float m_used = -INFINITY, l_run = 0.f;
-      int64_t shift = 0;  // the row's logits are taken at distance 0 of its segment's last query
+      int shift = 0;  // the row's logits are taken at distance 0 of its segment's last query
       int it = 0;
       for (unsigned ms = q.starts; ms && ok; ms &= ms - 1) {
-        const Segment sg = segment_at(p, q, __ffs(ms) - 1, lane);
+        const Segment sg = segment_at(p, q, __ffs(ms) - 1, lane, lm);
         // this row's keys in the segment's list: window lo .. hi - 1, entries n_w .. end - 1
         int lo = 0, hi = 0, end = 0;
         if (in && t >= 0 && qi >= sg.s && qi < sg.e) {
-          lo = static_cast<int>(window_start(t, p.n_win) - sg.wlo);
-          hi = static_cast<int>(t - sg.wlo) + 1;
-          end = sg.n_w + static_cast<int>(visible_entries(t, p.m, p.n_win));
+          lo = start32(p, t) - sg.wlo;
+          hi = t - sg.wlo + 1;
+          end = sg.n_w + visible32(p, t, lm);
           shift = t - sg.thi;
         }
         for (int k = 0; k < sg.ntiles; ++k, ++it) {
@@ -535,83 +751,112 @@ __global__ void __launch_bounds__(kThreads, 1)
                __all_sync(kFull, mbar_wait(&kfull[st], (gt / kNS) & 1u, p.status)) && !__any_sync(kFull, *sAbort != 0);
           if (!ok) break;
           tc_fence_after();
-          uint32_t s[kNk];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(sb + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * c));
-          tmem_ld_wait();
           const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk);
-          const uint64_t sl = pack2(slope2, slope2), pre = pack2(sl2, sl2);
+          const uint64_t sl = pack2(slope2, slope2);
+          // the tile in two halves of 64 keys (64 logits live at a time leave registers for the rule's eight in step);
+          // the second half's S is read while the first one's exponentials are taken
+          auto load = [&](int hf, uint32_t (&s)[64]) {
+            tmem_ld32(sb + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(s));
+            tmem_ld32(sb + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          };
+          auto rule = [&](int hf, uint32_t (&s)[64]) {
+            const float nr = m_used == -INFINITY ? 0.f : -m_used;
+            const uint64_t negref = pack2(nr, nr);
+            if constexpr (CAP) {
+              float big = 0.f, big1 = 0.f;
 #pragma unroll
-          for (int j = 0; j < kNk; j += 4) {
-            const float4 d = pos4[j / 4];
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const uint64_t bias = mul2(sl, e ? pack2(d.z, d.w) : pack2(d.x, d.y));
-              const uint64_t x = pack2(__uint_as_float(s[j + e]), __uint_as_float(s[j + e + 1]));
-              const uint64_t v = CAP ? capped2(x, pre, cap2, bias) : fma2(x, pre, bias);
-              float a, b;
-              unpack2(v, a, b);
-              s[j + e] = __float_as_uint(a);
-              s[j + e + 1] = __float_as_uint(b);
+              for (int j = 0; j < 64; j += 4) {
+                big = max3_abs(big, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+              }
+              if (__all_sync(kFull, fmaxf(big, big1) <= r.lim))
+                rule64<kPoly>(s, pos4 + 16 * hf, r, sl, negref);
+              else
+                rule64<kRational>(s, pos4 + 16 * hf, r, sl, negref);
+            } else {
+              rule64<kLinear>(s, pos4 + 16 * hf, r, sl, negref);
             }
-          }
-          const int a = k * kNk;
-          float mt = -INFINITY;
+          };
+          auto finish = [&](int hf, uint32_t (&s)[64]) {
+            float mt = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t vm = sMask[st * 4 + c] & (range_bits(a + 32 * c, lo, hi) | range_bits(a + 32 * c, sg.n_w, end));
-            if (__any_sync(kFull, vm != kFull)) {
+            for (int c = 0; c < 2; ++c) {
+              const int a = k * kNk + 64 * hf + 32 * c;
+              const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, sg.n_w, end));
+              if (__any_sync(kFull, vm != kFull)) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!((vm >> j) & 1u)) s[32 * c + j] = 0xff800000u;  // -inf
+                for (int j = 0; j < 32; ++j)
+                  if (!((vm >> j) & 1u)) s[32 * c + j] = 0xff800000u;  // -inf
+              }
+              float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                m0 = max3(m0, __uint_as_float(s[32 * c + j]), __uint_as_float(s[32 * c + j + 1]));
+                m1 = max3(m1, __uint_as_float(s[32 * c + j + 2]), __uint_as_float(s[32 * c + j + 3]));
+              }
+              mt = max3(mt, m0, m1);
             }
-            float m0 = -INFINITY, m1 = -INFINITY;
+            // the logits stand on the old maximum (0 before the row's first key); mt is their largest
+            const bool fresh = m_used == -INFINITY;
+            const bool up = mt > kRescaleThreshold || (fresh && mt != -INFINITY);
+            if (__any_sync(kFull, up)) {
+              const float delta = up ? mt : 0.f;
+              const float corr = up ? (fresh ? 0.f : ex2(-mt)) : 1.f;
+              l_run *= corr;
+              if (up) m_used = fresh ? mt : m_used + mt;
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              m0 = fmaxf(m0, __uint_as_float(s[32 * c + j]));
-              m1 = fmaxf(m1, __uint_as_float(s[32 * c + j + 1]));
-            }
-            mt = fmaxf(mt, fmaxf(m0, m1));
-          }
-          float corr = 1.f;
-          bool rescale = false;
-          if (mt > m_used + kRescaleThreshold || (m_used == -INFINITY && mt != -INFINITY)) {
-            corr = ex2(m_used - mt);  // 0 when m_used is -inf
-            rescale = it > 0;
-            l_run *= corr;
-            m_used = mt;
-          }
-          const float msub = m_used == -INFINITY ? 0.f : -m_used;
-          if (__any_sync(kFull, rescale)) {
+              for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - delta);
+              if (it > 0) {
 #pragma unroll 1
-            for (int c = 0; c < kD; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(ob + c, o);
-              tmem_ld_wait();
+                for (int c = 0; c < kD; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(ob + c, o);
+                  tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-              tmem_st16(ob + c, o);
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                  tmem_st16(ob + c, o);
+                }
+              }
+              if (hf > 0) {  // the first half's P stands on the old maximum too
+                tmem_st_wait();
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(sb + c, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    o[j] = pack_bf16(__uint_as_float(o[j] << 16) * corr, __uint_as_float(o[j] & 0xffff0000u) * corr);
+                  tmem_st16(sb + c, o);
+                }
+              }
             }
-          }
-          const uint64_t sub = pack2(msub, msub);
-          uint64_t l2 = pack2(0.f, 0.f);
+            uint64_t la = pack2(0.f, 0.f), lb = la;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pp[16];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pp[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float e0, e1;
-              unpack2(add2(pack2(__uint_as_float(s[32 * c + 2 * j]), __uint_as_float(s[32 * c + 2 * j + 1])), sub), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              l2 = add2(l2, pack2(e0, e1));
-              pp[j] = pack_bf16(e0, e1);
+              for (int j = 0; j < 16; ++j) {
+                const float e0 = ex2(__uint_as_float(s[32 * c + 2 * j])), e1 = ex2(__uint_as_float(s[32 * c + 2 * j + 1]));
+                if (j & 1) lb = add2(lb, pack2(e0, e1));
+                else la = add2(la, pack2(e0, e1));
+                pp[j] = pack_bf16(e0, e1);
+              }
+              tmem_st16(sb + 32 * hf + 16 * c, pp);
             }
-            tmem_st16(sb + 16 * c, pp);
-          }
-          float la, lb;
-          unpack2(l2, la, lb);
-          l_run += la + lb;
+            float l0, l1;
+            unpack2(add2(la, lb), l0, l1);
+            l_run += l0 + l1;
+          };
+          uint32_t s0[64], s1[64];
+          load(0, s0);
+          tmem_ld_wait();
+          rule(0, s0);
+          load(1, s1);
+          finish(0, s0);
+          tmem_ld_wait();
+          rule(1, s1);
+          finish(1, s1);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -627,78 +872,97 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool has = in && l_run > 0.f;
       const float inv = has ? 1.f / l_run : 0.f;
       float odd = 0.f;  // NaN once an output is not finite
-      auto put = [&](int c, const uint32_t (&o)[32]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            f[e] = has ? __uint_as_float(o[8 * i + e]) * inv : 0.f;
-            odd = fmaf(f[e], 0.f, odd);
-          }
-          if (p.rope_dims > 0 && has) {  // inverse RoPE of the output's last rope_dims channels
-            float a4[4] = {f[0], f[1], f[2], f[3]}, b4[4] = {f[4], f[5], f[6], f[7]};
-            inverse_rope4(a4, c + 8 * i, kD, p.rope_dims, p.rope_base, t);
-            inverse_rope4(b4, c + 8 * i + 4, kD, p.rope_dims, p.rope_base, t);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[e] = a4[e];
-              f[4 + e] = b4[e];
-            }
-          }
-          if (in)
-            *reinterpret_cast<uint4*>(p.out + row * kD + c + 8 * i) =
-                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+      const int tr = (warp & 3) * 32 + lane, first = item * kItemRows + w * kTileRows + (warp & 3) * 32;
+      uint8_t* obuf = sO + w * kHalfBytes + (warp & 3) * 32 * 128;  // this warp's 32 rows of 64 channels
+      // each warp's rows go out on their own, 64 channels at a time (rows past the last one are not written)
+      auto ship = [&](int hf) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && first < rows) {
+          tma_store_2d(&tm_out, hf * 64, first, obuf);
+          bulk_commit();
         }
       };
 #pragma unroll 1
-      for (int c = 0; c < kD; c += 32) {
-        uint32_t o[32];
-        if (ntot > 0) {
-          tmem_ld32(ob + c, o);
-          tmem_ld_wait();
-        }
-        put(c, o);
-      }
-      // the next item's first P V overwrites O: this warp's reads of it are complete
-      tc_fence_before();
-      __syncwarp();
-      if (ntot > 0 && lane == 0) mbar_arrive(&oread[w]);
-      float lse = has ? (m_used + log2f(l_run) - slope2 * static_cast<float>(shift)) * kLn2 : -INFINITY;
-      for (unsigned bad = __ballot_sync(kFull, in && (l_run != l_run || !(odd == 0.f))); bad; bad &= bad - 1) {
-        const int r = __ffs(bad) - 1;  // rows whose output is not finite, one at a time by the whole warp
-        const int64_t rr = __shfl_sync(kFull, row, r);
-        const int64_t tr = __shfl_sync(kFull, t, r);
-        float o4[4], m, l;
-        slow_row<CAP>(p, rr, sl2, cap2, __shfl_sync(kFull, slope2, r), o4, m, l, lane);
-        const float iv = 1.f / l;
+      for (int hf = 0; hf < 2; ++hf) {
+        if (lane == 0) bulk_wait_read();  // TMA has read what the buffer held
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t o[32];
+          if (ntot > 0) {
+            tmem_ld32(ob + 64 * hf + c, o);
+            tmem_ld_wait();
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o4[e] *= iv;
-        inverse_rope4(o4, 4 * lane, kD, p.rope_dims, p.rope_base, tr);
-        *reinterpret_cast<uint2*>(p.out + rr * kD + 4 * lane) = make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
-        if (lane == r) lse = (m + log2f(l)) * kLn2;
+          for (int i = 0; i < 4; ++i) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              f[e] = has ? __uint_as_float(o[8 * i + e]) * inv : 0.f;
+              odd = fmaf(f[e], 0.f, odd);
+            }
+            if (p.rope_dims > 0 && has) {  // inverse RoPE of the output's last rope_dims channels
+              float a4[4] = {f[0], f[1], f[2], f[3]}, b4[4] = {f[4], f[5], f[6], f[7]};
+              inverse_rope4(a4, 64 * hf + c + 8 * i, kD, p.rope_dims, p.rope_base, t);
+              inverse_rope4(b4, 64 * hf + c + 8 * i + 4, kD, p.rope_dims, p.rope_base, t);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                f[e] = a4[e];
+                f[4 + e] = b4[e];
+              }
+            }
+            *reinterpret_cast<uint4*>(obuf + lane * 128 + (((c / 8 + i) ^ (tr & 7)) << 4)) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+          }
+        }
+        if (hf == 1) {  // the next item's first P V overwrites O: this warp's reads of it are complete
+          tc_fence_before();
+          __syncwarp();
+          if (ntot > 0 && lane == 0) mbar_arrive(&oread[w]);
+        }
+        ship(hf);
+      }
+      float lse = has ? (m_used + log2f(l_run) - slope2 * static_cast<float>(shift)) * kLn2 : -INFINITY;
+      const unsigned bad = __ballot_sync(kFull, in && (l_run != l_run || !(odd == 0.f)));
+      if (bad) {  // rows to take again: TMA's stores of them are done first
+        if (lane == 0) bulk_wait();
+        __syncwarp();
+        for (unsigned left = bad; left; left &= left - 1) {
+          const int b = __ffs(left) - 1;  // one row at a time, by the whole warp
+          const int rr = __shfl_sync(kFull, row, b);
+          float o4[4], m, l;
+          slow_row<CAP>(p, rr, r.pre, r.cap2, __shfl_sync(kFull, slope2, b), o4, m, l, lane);
+          const float iv = 1.f / l;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o4[e] *= iv;
+          inverse_rope4(o4, 4 * lane, kD, p.rope_dims, p.rope_base, __shfl_sync(kFull, t, b));
+          *reinterpret_cast<uint2*>(p.out + (int64_t)rr * kD + 4 * lane) =
+              make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
+          if (lane == b) lse = (m + log2f(l)) * kLn2;
+        }
       }
       if (in && p.lse) p.lse[row] = lse;
       g += ntot;
       if (ntot > 0) ++n_act;
     }
     if (!ok) *sAbort = 1;
+    if (lane == 0) bulk_wait();
   }
   cp_async_wait<0>();
-  // after an abort, a Q copy in flight gets a bounded chance to land
-  if (warp == 9 && __shfl_sync(kFull, *sAbort, 0)) mbar_wait(qfull, n_act & 1u, nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, kTmemCols);
 }
 
-bool encode_q(CUtensorMap* map, const void* base, uint64_t rows) {
+// rows of 128 channels in 64-channel boxes of box_rows rows, 128-byte swizzle
+bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kTileRows)};
+  const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -714,20 +978,28 @@ bool attend_chunk_supported(const AttendParams& p, int n_sm) {
   const int64_t rows = (int64_t)p.n_q * p.n_heads;
   return !p.is_csa && has_score_rule(p) && p.x_chunk && p.d_qk == kD && p.d_v == kD && p.n_heads >= 16 &&
          p.kv_dtype == CSKV_BF16 && rows >= (int64_t)kItemRows * n_sm / 2 && rows <= 0x7fffffff - kItemRows &&
-         visible_entries(p.max_pos, p.m, p.n_win) < (1 << 29) && p.n_win < (1 << 29) &&
+         p.max_pos < (1 << 30) && p.n_win < (1 << 30) && p.chunk_len > 0 &&
          pool_rows <= kRowMask && ring_rows <= kRowMask && static_cast<uint64_t>(p.chunk_len) <= kRowMask;
 }
 
 cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
-  CUtensorMap tm_q;
+  CUtensorMap tm_q, tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, tm_out;
   const int64_t rows = (int64_t)p.n_q * p.n_heads;
-  if (!encode_q(&tm_q, p.q, static_cast<uint64_t>(rows))) return cudaErrorNotSupported;
+  const uint64_t pool_rows = static_cast<uint64_t>(p.n_pages) * p.page_size;
+  const uint64_t ring_rows = static_cast<uint64_t>(p.n_seqs_layer) * p.n_win;
+  const uint64_t chunk_rows = static_cast<uint64_t>(p.chunk_len);
+  if (!encode_rows(&tm_q, p.q, rows, kTileRows) || !encode_rows(&tm_out, p.out, rows, 32) ||
+      !encode_rows(&tm_pool, p.kv_pool, pool_rows, 1) || !encode_rows(&tm_pool16, p.kv_pool, pool_rows, 16) ||
+      !encode_rows(&tm_ring, p.ring_x, ring_rows, 1) || !encode_rows(&tm_ring16, p.ring_x, ring_rows, 16) ||
+      !encode_rows(&tm_chunk, p.x_chunk, chunk_rows, 1) || !encode_rows(&tm_chunk16, p.x_chunk, chunk_rows, 16))
+    return cudaErrorNotSupported;
   const size_t smem = Smem::bytes();
   auto kern = p.score_cap > 0.f ? attend_chunk_kernel<true> : attend_chunk_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int64_t items = (rows + kItemRows - 1) / kItemRows;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q,
+                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, tm_out, p);
 }
 
 }  // namespace cskv
