@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // a shuffle from a constant lane is what the compiler takes as the same value in every lane
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNS; ++i) {
       mbar_init(&kfull[i], 2);
@@ -468,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sTmem;
+  const uint32_t tmem = __shfl_sync(kFull, *sTmem, 0);
   grid_dependency_wait();
   grid_dependents_launch();
   if (blockIdx.x == 0)
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       RawQuery raw = fetch_query(p, item, lane);
       auto next_tiles = [&]() {  // key tiles of the next item that has any, 0 at the end
         for (; item < n_items;) {
-          const int n = item_tiles(p, item_queries(p, item, raw, lane), lane, lm);
+          const int n = __shfl_sync(kFull, item_tiles(p, item_queries(p, item, raw, lane), lane, lm), 0);
           item += gridDim.x;
           raw = fetch_query(p, item, lane);
           if (n) return n;
