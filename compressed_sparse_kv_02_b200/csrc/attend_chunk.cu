@@ -13,12 +13,16 @@
 // with P written as bf16 over S in tensor memory (the A operand of P V) and V read
 // MN-major from the key tile. The two tiles alternate on the tensor cores: while
 // one's softmax runs, the other's P V and next S do.
-//   warps 0-3, 4-7: softmax of tile 0 / 1, one row per thread; O is rescaled only
-//     when the row max rises by more than 2^8. O goes out through shared memory
-//     and TMA (written by the threads, 32 rows per instruction, it took 8,700
-//     cycles per item);
-//   warp 8: issues the MMAs;
-//   warps 9, 10: look up the keys' rows, four keys per lane, and have TMA copy the
+//   warps 0-15: softmax, two threads per row: warps 8 w + 4 h .. + 3 take keys
+//     64 h .. + 63 of tile w. (One thread per row, with two softmax warps on a
+//     scheduler, waited for its own instructions most of the time: 198.9 us where
+//     this takes NEW us.) The two agree on the row's reference maximum at a barrier,
+//     which moves only when a logit exceeds it by more than 2^8; O is rescaled
+//     then, half of its channels by each. O goes out through shared memory and TMA
+//     (written by the threads, 32 rows per instruction, it took 8,700 cycles per
+//     item);
+//   warp 16: issues the MMAs;
+//   warps 17, 18: look up the keys' rows, four keys per lane, and have TMA copy the
 //     two 64-channel halves of each tile: 16 consecutive rows per copy where a run
 //     of 16 keys has them, else gathers of four rows. A copy costs its warp ~150
 //     cycles whatever its size: 64 gathers by one warp took 10,000 cycles per tile,
@@ -56,7 +60,9 @@ constexpr int kNk = 128;                     // keys per tile
 constexpr int kNS = 3;                       // key stages
 constexpr int kHalfBytes = kNk * 128;        // 16384: one 64-channel half of 128 rows
 constexpr int kStageBytes = 2 * kHalfBytes;  // 32768 (also one Q tile)
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kMmaWarp = 16, kLoadWarp0 = 17;
+constexpr int kTileThreads = 256;            // softmax threads of one tile
 constexpr int kMaxStep = 32;                 // largest step between positions of one segment's queries
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w (P over its first 64 columns), O at 256 + 128 w
@@ -67,11 +73,12 @@ constexpr float kRescaleThreshold = 8.0f;    // log2 units
 struct Smem {
   static constexpr int Q = 0;
   static constexpr int K = Q + 2 * kStageBytes;
-  static constexpr int OUT = K + kNS * kStageBytes;   // 64 output channels of both tiles on their way to TMA
+  static constexpr int OUT = K + kNS * kStageBytes;   // 32 channels of each softmax warp's rows on their way to TMA
   static constexpr int POS = OUT + 2 * kHalfBytes;    // [kNS][kNk] key positions relative to the segment's last query
   static constexpr int ROWS = POS + kNS * kNk * 4;    // [2][kNk] source-row codes (a tile copied by cp.async)
   static constexpr int MASK = ROWS + 2 * kNk * 4;         // [kNS][4] valid-key bits
-  static constexpr int BAR = MASK + kNS * 16;
+  static constexpr int SIDE = MASK + kNS * 16;        // [2 tiles][2 halves][128 rows] maxima and sums the halves exchange
+  static constexpr int BAR = SIDE + 4 * kTileRows * 4;
   static constexpr int TMEM = BAR + 24 * 8;
   static constexpr int FLAGS = TMEM + 8;
   static constexpr int END = FLAGS + 8;
@@ -181,6 +188,16 @@ __device__ __forceinline__ uint32_t range_bits(int a, int lo, int hi) {
   return h > l ? (0xffffffffu >> (32 - (h - l))) << l : 0u;
 }
 
+// named barrier over n threads that also returns the OR of `v` over them (the same in every thread)
+__device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred q, p;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
 // The MMAs are issued by one elected lane, but by code that the whole warp runs together: the descriptors then sit in
 // uniform registers. Inside a branch on the lane every one of them is moved there first, which held an MMA up for
 // ~140 cycles (64 is what it takes to run).
@@ -224,30 +241,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
-// ---------------------------------------------------------------- packed fp32 pairs
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
@@ -268,104 +261,106 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // cap tanh(s pre) as a polynomial in s where |s pre| <= 1, to a relative error of 6e-7: tanh(u) / u in u^2 on [0, 1]
 // (fitted like tanh_rational), its coefficients times cap2 pre^(2i + 1). Logits seldom reach the cap, so most tiles
 // take this form: 7 fp32 operations a logit instead of 12, and no reciprocal.
-__device__ constexpr float tanh_p(int i) {
-  return i == 0 ? 0.9999994039535522f : i == 1 ? -0.3332904279232025f : i == 2 ? 0.13281434774398804f
-                      : i == 3 ? -0.051605693995952606f : i == 4 ? 0.016743136569857597f : -0.0030670680571347475f;
-}
+constexpr float kTanhP[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281434774398804f,
+                             -0.051605693995952606f, 0.016743136569857597f, -0.0030670680571347475f};
+// The rule's numbers, as a kernel argument: packed arithmetic then reads its constants, each a pair of the same number,
+// where they are instead of building the pairs in registers.
 struct Rule {
-  float pre, cap2;  // capped: sm_scale / cap and cap log2(e); else sm_scale log2(e) and 0
-  float lim;        // |s| up to here takes the polynomial (negative: never)
-  float c[6];
+  float2 pre, cap2;  // capped: sm_scale / cap and cap log2(e); else sm_scale log2(e) and 0
+  float2 c[6];
+  float lim;         // |s| up to here takes the polynomial (negative: never)
 };
-__device__ __forceinline__ Rule make_rule(const AttendParams& p, bool cap) {
+Rule make_rule(const AttendParams& p) {
+  const bool cap = p.score_cap > 0.f;
   Rule r;
-  r.cap2 = cap ? p.score_cap * kLog2e : 0.f;
-  r.pre = cap ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
-  r.lim = r.pre < 2048.f ? 1.f / r.pre : -1.f;  // above that pre^10 would leave fp32's range
-  float f = r.cap2 * r.pre;
-#pragma unroll
+  const float pre = cap ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e, cap2 = cap ? p.score_cap * kLog2e : 0.f;
+  r.pre = make_float2(pre, pre);
+  r.cap2 = make_float2(cap2, cap2);
+  r.lim = pre < 2048.f ? 1.f / pre : -1.f;  // above that pre^10 would leave fp32's range
+  float f = cap2 * pre;
   for (int i = 0; i < 6; ++i) {
-    r.c[i] = f * tanh_p(i);
-    f *= r.pre * r.pre;
+    r.c[i] = make_float2(f * kTanhP[i], f * kTanhP[i]);
+    f *= pre * pre;
   }
   return r;
 }
 
-// The rule on 64 logits, packed pairs of four at a time in step: with the cap, without, or capped below lim. bias =
-// slope2 * position - ref, ref the row's running maximum so far (its subtraction costs nothing here). Independent
-// chains in step keep a scheduler with two softmax warps issuing (pair after pair left it idle 2/3 of the time).
+// The rule on 64 logits, two packed pairs in step: with the cap, without, or capped below lim. bias = slope2 * position
+// - ref, ref the row's running maximum so far (its subtraction costs nothing here).
 enum { kLinear, kRational, kPoly };
 template <int FORM>
-__device__ __forceinline__ void rule64(uint32_t (&s)[64], const float4* pos, const Rule& r, uint64_t slope,
-                                       uint64_t negref) {
-  const uint64_t pre = pack2(r.pre, r.pre), cap2 = pack2(r.cap2, r.cap2);
+__device__ __forceinline__ void rule64(uint32_t (&s)[64], const float4* pos, const Rule& r, float2 slope,
+                                       float2 negref) {
 #pragma unroll
-  for (int b = 0; b < 64; b += 8) {
-    const float4 pa = pos[b / 4], pb = pos[b / 4 + 1];
-    uint64_t u[4], bias[4] = {fma2(slope, pack2(pa.x, pa.y), negref), fma2(slope, pack2(pa.z, pa.w), negref),
-                              fma2(slope, pack2(pb.x, pb.y), negref), fma2(slope, pack2(pb.z, pb.w), negref)};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = pack2(__uint_as_float(s[b + 2 * j]), __uint_as_float(s[b + 2 * j + 1]));
+  for (int b = 0; b < 64; b += 4) {
+    const float4 pa = pos[b / 4];
+    float2 u[2] = {make_float2(__uint_as_float(s[b]), __uint_as_float(s[b + 1])),
+                   make_float2(__uint_as_float(s[b + 2]), __uint_as_float(s[b + 3]))};
+    const float2 bias[2] = {__ffma2_rn(slope, make_float2(pa.x, pa.y), negref), __ffma2_rn(slope, make_float2(pa.z, pa.w), negref)};
     if constexpr (FORM == kLinear) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = fma2(u[j], pre, bias[j]);
+      for (int j = 0; j < 2; ++j) u[j] = __ffma2_rn(u[j], r.pre, bias[j]);
     } else if constexpr (FORM == kPoly) {
-      uint64_t x[4], n[4];
+      float2 x[2], n[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], u[j]);
+      for (int j = 0; j < 2; ++j) x[j] = __fmul2_rn(u[j], u[j]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) n[j] = fma2(pack2(r.c[5], r.c[5]), x[j], pack2(r.c[4], r.c[4]));
+      for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(r.c[5], x[j], r.c[4]);
 #pragma unroll
       for (int i = 3; i >= 0; --i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) n[j] = fma2(n[j], x[j], pack2(r.c[i], r.c[i]));
+        for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(n[j], x[j], r.c[i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = fma2(u[j], n[j], bias[j]);
+      for (int j = 0; j < 2; ++j) u[j] = __ffma2_rn(u[j], n[j], bias[j]);
     } else {
-      uint64_t x[4], n[4], d[4];
+      float2 x[2], n[2], d[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] = mul2(u[j], pre);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float u0, u1;
-        unpack2(u[j], u0, u1);
-        u[j] = pack2(tanh_clamp(u0), tanh_clamp(u1));
+      for (int j = 0; j < 2; ++j) {
+        u[j] = __fmul2_rn(u[j], r.pre);
+        u[j] = make_float2(tanh_clamp(u[j].x), tanh_clamp(u[j].y));
+        x[j] = __fmul2_rn(u[j], u[j]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = mul2(u[j], u[j]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) d[j] = fma2(pack2(tanh_d(4), tanh_d(4)), x[j], pack2(tanh_d(3), tanh_d(3)));
+      for (int j = 0; j < 2; ++j) d[j] = __ffma2_rn(make_float2(tanh_d(4), tanh_d(4)), x[j], make_float2(tanh_d(3), tanh_d(3)));
 #pragma unroll
       for (int i = 2; i >= 0; --i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = fma2(d[j], x[j], pack2(tanh_d(i), tanh_d(i)));
+        for (int j = 0; j < 2; ++j) d[j] = __ffma2_rn(d[j], x[j], make_float2(tanh_d(i), tanh_d(i)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) n[j] = fma2(pack2(tanh_n(3), tanh_n(3)), x[j], pack2(tanh_n(2), tanh_n(2)));
+      for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(make_float2(tanh_n(3), tanh_n(3)), x[j], make_float2(tanh_n(2), tanh_n(2)));
 #pragma unroll
       for (int i = 1; i >= 0; --i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) n[j] = fma2(n[j], x[j], pack2(tanh_n(i), tanh_n(i)));
+        for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(n[j], x[j], make_float2(tanh_n(i), tanh_n(i)));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) n[j] = mul2(n[j], u[j]);
+      for (int j = 0; j < 2; ++j) n[j] = __fmul2_rn(n[j], u[j]);
       // two quotients share one reciprocal: 1 / d_a = d_b / (d_a d_b), each d at most 2^7.3
-#pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        float q0, q1, r0, r1;
-        unpack2(mul2(d[j], d[j + 1]), q0, q1);
-        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r0) : "f"(q0));
-        asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r1) : "f"(q1));
-        const uint64_t rc = mul2(pack2(r0, r1), cap2);
-        u[j] = fma2(mul2(n[j], d[j + 1]), rc, bias[j]);
-        u[j + 1] = fma2(mul2(n[j + 1], d[j]), rc, bias[j + 1]);
-      }
+      const float2 dd = __fmul2_rn(d[0], d[1]);
+      float2 rc;
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(rc.x) : "f"(dd.x));
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(rc.y) : "f"(dd.y));
+      rc = __fmul2_rn(rc, r.cap2);
+      u[0] = __ffma2_rn(__fmul2_rn(n[0], d[1]), rc, bias[0]);
+      u[1] = __ffma2_rn(__fmul2_rn(n[1], d[0]), rc, bias[1]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float a, c;
-      unpack2(u[j], a, c);
-      s[b + 2 * j] = __float_as_uint(a);
-      s[b + 2 * j + 1] = __float_as_uint(c);
+    for (int j = 0; j < 2; ++j) {
+      s[b + 2 * j] = __float_as_uint(u[j].x);
+      s[b + 2 * j + 1] = __float_as_uint(u[j].y);
     }
+  }
+}
+
+// Inverse RoPE of 16 output channels ch0 .. ch0 + 15, out of the way of the registers of its caller
+__device__ __noinline__ void rope16(uint32_t (&o)[16], int ch0, const AttendParams& p, int t) {
+#pragma unroll 1
+  for (int i = 0; i < 16; i += 4) {
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(o[i + e]);
+    inverse_rope4(f, ch0 + i, kD, p.rope_dims, p.rope_base, t);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i + e] = __float_as_uint(f[e]);
   }
 }
 
@@ -418,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_ring, const __grid_constant__ CUtensorMap tm_chunk,
                         const __grid_constant__ CUtensorMap tm_pool16, const __grid_constant__ CUtensorMap tm_ring16,
                         const __grid_constant__ CUtensorMap tm_chunk16, const __grid_constant__ CUtensorMap tm_out,
-                        const __grid_constant__ AttendParams p) {
+                        const __grid_constant__ AttendParams p, const __grid_constant__ Rule r) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Smem::Q;
@@ -427,12 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sPos = reinterpret_cast<float*>(sm + Smem::POS);
   uint32_t* sRow = reinterpret_cast<uint32_t*>(sm + Smem::ROWS);
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
+  float* sSide = reinterpret_cast<float*>(sm + Smem::SIDE);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + Smem::BAR);  // [3] loaders (2) -> MMA, softmax
   uint64_t* kempty = kfull + kNS;                                 // [3] MMA -> loaders
   uint64_t* sfull = kempty + kNS;                                 // [2] MMA -> softmax
-  uint64_t* pfull = sfull + 2;                                    // [2] softmax (4 warps) -> MMA
+  uint64_t* pfull = sfull + 2;                                    // [2] softmax (8 warps) -> MMA
   uint64_t* odone = pfull + 2;                                    // [2] MMA -> softmax
-  uint64_t* oread = odone + 2;                                    // [2] softmax (4 warps) -> MMA
+  uint64_t* oread = odone + 2;                                    // [2] softmax (8 warps) -> MMA
   uint64_t* qfull = oread + 2;                                    // [2] Q of the tile landed (TMA)
   uint64_t* qempty = qfull + 2;                                   // [2] the item's S products of the tile are done
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
@@ -447,22 +443,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[i], 8);
       mbar_init(&odone[i], 1);
-      mbar_init(&oread[i], 4);
+      mbar_init(&oread[i], 8);
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], 1);
     }
     fence_barrier_init();
     *sAbort = 0;
   }
-  if (tid == 288) {
+  if (tid == 32 * kLoadWarp0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_pool16);
     prefetch_tensormap(&tm_chunk16);
     prefetch_tensormap(&tm_out);
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tmem_alloc(sTmem, kTmemCols);
     tmem_relinquish();
   }
@@ -486,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t g = 0;      // key tiles before the current item
   uint32_t n_act = 0;  // items with keys before the current one
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-    if (warp == 8) {
+  if (warp >= kMmaWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issue (lane 0; the warp waits together)
       const uint32_t issuer = elect_one();
       constexpr uint32_t idesc_s = umma_idesc_bf16(kTileRows, kNk, false);
@@ -590,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         mbar_wait(&odone[0], n_act & 1u, nullptr);
       }
-    } else if (warp < 11) {
+    } else if (warp < kLoadWarp0 + 2) {
       // ---------------------------------------------------------------- loaders (a warp per channel half and Q tile)
-      const int half = warp - 9;
+      const int half = warp - kLoadWarp0;
       bool ok = true;
       uint32_t issued = 0, q_issued = 0;  // key tiles and Q loads given to TMA
       RawQuery raw = fetch_query(p, blockIdx.x, lane);
@@ -712,24 +708,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ------------------------------------------------------------------ softmax (one row per thread)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
-    const int w = warp >> 2;
+    // ------------------------------------------------------------------ softmax (half a row per thread)
+    // Every softmax warp of a tile reaches the tile's barriers; a bounded wait that gave up only marks the tile bad,
+    // and a barrier's OR decides for all of them.
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    const int w = warp >> 3, hf = (warp >> 2) & 1, tr = (warp & 3) * 32 + lane;  // tile, key half, row of the tile
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t sb = trow + kColS + w * kNk, ob = trow + kColO + w * kD;
-    const Rule r = make_rule(p, CAP);
+    // S of my keys; P of a tile lies over the first half of its S; O of my channels
+    const uint32_t sb = trow + kColS + w * kNk + 64 * hf, pb = trow + kColS + w * kNk + 32 * hf;
+    const uint32_t ob = trow + kColO + w * kD + 64 * hf;
+    float* side = sSide + (2 * w + hf) * kTileRows + tr;
+    float* other = sSide + (2 * w + (hf ^ 1)) * kTileRows + tr;
+    uint8_t* obuf = sO + warp * 2048;  // this warp's 32 rows of 32 channels
     bool ok = true;
     RawQuery raw = fetch_query(p, blockIdx.x, lane);
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
       const Queries q = item_queries(p, item, raw, lane);
       raw = fetch_query(p, item + gridDim.x, lane);
-      const int row = item * kItemRows + w * kTileRows + (warp & 3) * 32 + lane;
+      const int row = item * kItemRows + w * kTileRows + tr;
       const bool in = row < rows;
       const int qi = in ? row / p.n_heads - q.q0 : 0;  // this row's query lane
-      const int h = in ? row % p.n_heads : 0;
       const int t = __shfl_sync(kFull, q.t, qi);
-      const float slope2 = p.slopes ? p.slopes[h] * kLog2e : 0.f;
-      const int ntot = item_tiles(p, q, lane, lm);
+      const float slope2 = p.slopes && in ? p.slopes[row % p.n_heads] * kLog2e : 0.f;
       float m_used = -INFINITY, l_run = 0.f;
       int shift = 0;  // the row's logits are taken at distance 0 of its segment's last query
       int it = 0;
@@ -748,21 +748,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = gt % kNS;
           // the stage's positions and key bits were written before kfull; that phase cannot move on before this
           // thread's P has been used
-          ok = __all_sync(kFull, mbar_wait(&sfull[w], gt & 1u, p.status)) &&
-               __all_sync(kFull, mbar_wait(&kfull[st], (gt / kNS) & 1u, p.status)) && !__any_sync(kFull, *sAbort != 0);
-          if (!ok) break;
+          bool good = __all_sync(kFull, mbar_wait(&sfull[w], gt & 1u, p.status)) &&
+                      __all_sync(kFull, mbar_wait(&kfull[st], (gt / kNS) & 1u, p.status));
           tc_fence_after();
-          const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk);
-          const uint64_t sl = pack2(slope2, slope2);
-          // the tile in two halves of 64 keys (64 logits live at a time leave registers for the rule's eight in step);
-          // the second half's S is read while the first one's exponentials are taken
-          auto load = [&](int hf, uint32_t (&s)[64]) {
-            tmem_ld32(sb + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(s));
-            tmem_ld32(sb + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-          };
-          auto rule = [&](int hf, uint32_t (&s)[64]) {
+          uint32_t s[64];
+          tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
+          tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+          tmem_ld_wait();
+          {
             const float nr = m_used == -INFINITY ? 0.f : -m_used;
-            const uint64_t negref = pack2(nr, nr);
+            const float2 negref = make_float2(nr, nr), sl = make_float2(slope2, slope2);
+            const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf);
             if constexpr (CAP) {
               float big = 0.f, big1 = 0.f;
 #pragma unroll
@@ -771,93 +767,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                 big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
               }
               if (__all_sync(kFull, fmaxf(big, big1) <= r.lim))
-                rule64<kPoly>(s, pos4 + 16 * hf, r, sl, negref);
+                rule64<kPoly>(s, pos4, r, sl, negref);
               else
-                rule64<kRational>(s, pos4 + 16 * hf, r, sl, negref);
+                rule64<kRational>(s, pos4, r, sl, negref);
             } else {
-              rule64<kLinear>(s, pos4 + 16 * hf, r, sl, negref);
+              rule64<kLinear>(s, pos4, r, sl, negref);
             }
-          };
-          auto finish = [&](int hf, uint32_t (&s)[64]) {
-            float mt = -INFINITY;
+          }
+          float mt = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int a = k * kNk + 64 * hf + 32 * c;
-              const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, sg.n_w, end));
-              if (__any_sync(kFull, vm != kFull)) {
+          for (int c = 0; c < 2; ++c) {
+            const int a = k * kNk + 64 * hf + 32 * c;
+            const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, sg.n_w, end));
+            if (__any_sync(kFull, vm != kFull)) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!((vm >> j) & 1u)) s[32 * c + j] = 0xff800000u;  // -inf
-              }
-              float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                m0 = max3(m0, __uint_as_float(s[32 * c + j]), __uint_as_float(s[32 * c + j + 1]));
-                m1 = max3(m1, __uint_as_float(s[32 * c + j + 2]), __uint_as_float(s[32 * c + j + 3]));
-              }
-              mt = max3(mt, m0, m1);
+              for (int j = 0; j < 32; ++j)
+                if (!((vm >> j) & 1u)) s[32 * c + j] = 0xff800000u;  // -inf
             }
-            // the logits stand on the old maximum (0 before the row's first key); mt is their largest
-            const bool fresh = m_used == -INFINITY;
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              m0 = max3(m0, __uint_as_float(s[32 * c + j]), __uint_as_float(s[32 * c + j + 1]));
+              m1 = max3(m1, __uint_as_float(s[32 * c + j + 2]), __uint_as_float(s[32 * c + j + 3]));
+            }
+            mt = max3(mt, m0, m1);
+          }
+          // The logits stand on the old maximum (0 before the row's first key). Both halves of the tile's rows have
+          // read S once they meet here, so P may be written over it.
+          const bool fresh = m_used == -INFINITY;
+          const bool bad = !good || *sAbort != 0;
+          if (named_sync_or(1 + w, kTileThreads, bad || mt > kRescaleThreshold || (fresh && mt != -INFINITY))) {
+            *side = mt;
+            if (named_sync_or(1 + w, kTileThreads, bad)) {
+              ok = false;
+              break;
+            }
+            mt = fmaxf(mt, *other);
             const bool up = mt > kRescaleThreshold || (fresh && mt != -INFINITY);
-            if (__any_sync(kFull, up)) {
-              const float delta = up ? mt : 0.f;
-              const float corr = up ? (fresh ? 0.f : ex2(-mt)) : 1.f;
-              l_run *= corr;
-              if (up) m_used = fresh ? mt : m_used + mt;
+            const float delta = up ? mt : 0.f;
+            const float corr = up ? (fresh ? 0.f : ex2(-mt)) : 1.f;
+            l_run *= corr;
+            if (up) m_used = fresh ? mt : m_used + mt;
 #pragma unroll
-              for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - delta);
-              if (it > 0) {
+            for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - delta);
+            if (it > 0) {
 #pragma unroll 1
-                for (int c = 0; c < kD; c += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(ob + c, o);
-                  tmem_ld_wait();
+              for (int c = 0; c < 64; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(ob + c, o);
+                tmem_ld_wait();
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
-                  tmem_st16(ob + c, o);
-                }
-              }
-              if (hf > 0) {  // the first half's P stands on the old maximum too
-                tmem_st_wait();
-#pragma unroll 1
-                for (int c = 0; c < 32; c += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(sb + c, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int j = 0; j < 16; ++j)
-                    o[j] = pack_bf16(__uint_as_float(o[j] << 16) * corr, __uint_as_float(o[j] & 0xffff0000u) * corr);
-                  tmem_st16(sb + c, o);
-                }
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * corr);
+                tmem_st16(ob + c, o);
               }
             }
-            uint64_t la = pack2(0.f, 0.f), lb = la;
+          }
+          float2 la = make_float2(0.f, 0.f), lb = la;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pp[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pp[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float e0 = ex2(__uint_as_float(s[32 * c + 2 * j])), e1 = ex2(__uint_as_float(s[32 * c + 2 * j + 1]));
-                if (j & 1) lb = add2(lb, pack2(e0, e1));
-                else la = add2(la, pack2(e0, e1));
-                pp[j] = pack_bf16(e0, e1);
-              }
-              tmem_st16(sb + 32 * hf + 16 * c, pp);
+            for (int j = 0; j < 16; ++j) {
+              const float e0 = ex2(__uint_as_float(s[32 * c + 2 * j])), e1 = ex2(__uint_as_float(s[32 * c + 2 * j + 1]));
+              if (j & 1) lb = __fadd2_rn(lb, make_float2(e0, e1));
+              else la = __fadd2_rn(la, make_float2(e0, e1));
+              pp[j] = pack_bf16(e0, e1);
             }
-            float l0, l1;
-            unpack2(add2(la, lb), l0, l1);
-            l_run += l0 + l1;
-          };
-          uint32_t s0[64], s1[64];
-          load(0, s0);
-          tmem_ld_wait();
-          rule(0, s0);
-          load(1, s1);
-          finish(0, s0);
-          tmem_ld_wait();
-          rule(1, s1);
-          finish(1, s1);
+            tmem_st16(pb + 16 * c, pp);
+          }
+          la = __fadd2_rn(la, lb);
+          l_run += la.x + la.y;
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
@@ -865,87 +844,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // epilogue: O / l in bf16, and the log-sum-exp
-      if (ntot > 0) {
-        if (!(ok = __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status)))) break;
-        tc_fence_after();
+      // epilogue: O / l in bf16 (64 channels per thread), and the log-sum-exp
+      *side = l_run;
+      const bool done = it == 0 || __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status));
+      tc_fence_after();
+      if (named_sync_or(1 + w, kTileThreads, !done)) {
+        ok = false;
+        break;
       }
+      l_run += *other;
       const bool has = in && l_run > 0.f;
       const float inv = has ? 1.f / l_run : 0.f;
-      float odd = 0.f;  // NaN once an output is not finite
-      const int tr = (warp & 3) * 32 + lane, first = item * kItemRows + w * kTileRows + (warp & 3) * 32;
-      uint8_t* obuf = sO + w * kHalfBytes + (warp & 3) * 32 * 128;  // this warp's 32 rows of 64 channels
-      // each warp's rows go out on their own, 64 channels at a time (rows past the last one are not written)
-      auto ship = [&](int hf) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && first < rows) {
-          tma_store_2d(&tm_out, hf * 64, first, obuf);
-          bulk_commit();
-        }
-      };
+      const int first = row - lane;  // of this warp's rows
+      float odd = 0.f;               // NaN once an output is not finite
 #pragma unroll 1
-      for (int hf = 0; hf < 2; ++hf) {
+      for (int c = 0; c < 64; c += 32) {
         if (lane == 0) bulk_wait_read();  // TMA has read what the buffer held
         __syncwarp();
 #pragma unroll 1
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t o[32];
-          if (ntot > 0) {
-            tmem_ld32(ob + 64 * hf + c, o);
+        for (int i = 0; i < 2; ++i) {
+          uint32_t o[16];
+          if (it > 0) {
+            tmem_ld16(ob + c + 16 * i, o);
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float f[8];
+          for (int e = 0; e < 16; ++e) {
+            o[e] = has ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+            odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
+          }
+          // inverse RoPE of the output's last rope_dims channels
+          if (p.rope_dims > 0 && has) rope16(o, 64 * hf + c + 16 * i, p, t);
+          // 64-byte rows, 16-byte pieces swizzled by address bits 7 and 8
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              f[e] = has ? __uint_as_float(o[8 * i + e]) * inv : 0.f;
-              odd = fmaf(f[e], 0.f, odd);
-            }
-            if (p.rope_dims > 0 && has) {  // inverse RoPE of the output's last rope_dims channels
-              float a4[4] = {f[0], f[1], f[2], f[3]}, b4[4] = {f[4], f[5], f[6], f[7]};
-              inverse_rope4(a4, 64 * hf + c + 8 * i, kD, p.rope_dims, p.rope_base, t);
-              inverse_rope4(b4, 64 * hf + c + 8 * i + 4, kD, p.rope_dims, p.rope_base, t);
+          for (int e = 0; e < 2; ++e) {
+            uint32_t v[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                f[e] = a4[e];
-                f[4 + e] = b4[e];
-              }
-            }
-            *reinterpret_cast<uint4*>(obuf + lane * 128 + (((c / 8 + i) ^ (tr & 7)) << 4)) =
-                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+            for (int j = 0; j < 4; ++j)
+              v[j] = pack_bf16(__uint_as_float(o[8 * e + 2 * j]), __uint_as_float(o[8 * e + 2 * j + 1]));
+            *reinterpret_cast<uint4*>(obuf + lane * 64 + (((2 * i + e) ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
-        if (hf == 1) {  // the next item's first P V overwrites O: this warp's reads of it are complete
-          tc_fence_before();
-          __syncwarp();
-          if (ntot > 0 && lane == 0) mbar_arrive(&oread[w]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && first < rows) {  // rows past the last one are not written
+          tma_store_2d(&tm_out, 64 * hf + c, first, obuf);
+          bulk_commit();
         }
-        ship(hf);
       }
+      // the next item's first P V overwrites O: this warp's reads of it are complete
+      tc_fence_before();
+      __syncwarp();
+      if (it > 0 && lane == 0) mbar_arrive(&oread[w]);
       float lse = has ? (m_used + log2f(l_run) - slope2 * static_cast<float>(shift)) * kLn2 : -INFINITY;
-      const unsigned bad = __ballot_sync(kFull, in && (l_run != l_run || !(odd == 0.f)));
-      if (bad) {  // rows to take again: TMA's stores of them are done first
+      const unsigned redo = __ballot_sync(kFull, in && (l_run != l_run || !(odd == 0.f)));
+      if (redo) {  // rows to take again (my channels of them): TMA's stores of them are done first
         if (lane == 0) bulk_wait();
         __syncwarp();
-        for (unsigned left = bad; left; left &= left - 1) {
+        for (unsigned left = redo; left; left &= left - 1) {
           const int b = __ffs(left) - 1;  // one row at a time, by the whole warp
           const int rr = __shfl_sync(kFull, row, b);
           float o4[4], m, l;
-          slow_row<CAP>(p, rr, r.pre, r.cap2, __shfl_sync(kFull, slope2, b), o4, m, l, lane);
+          slow_row<CAP>(p, rr, r.pre.x, r.cap2.x, __shfl_sync(kFull, slope2, b), o4, m, l, lane);
           const float iv = 1.f / l;
 #pragma unroll
           for (int e = 0; e < 4; ++e) o4[e] *= iv;
           inverse_rope4(o4, 4 * lane, kD, p.rope_dims, p.rope_base, __shfl_sync(kFull, t, b));
-          *reinterpret_cast<uint2*>(p.out + (int64_t)rr * kD + 4 * lane) =
-              make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
+          if (lane >> 4 == hf)
+            *reinterpret_cast<uint2*>(p.out + (int64_t)rr * kD + 4 * lane) =
+                make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
           if (lane == b) lse = (m + log2f(l)) * kLn2;
         }
       }
-      if (in && p.lse) p.lse[row] = lse;
-      g += ntot;
-      if (ntot > 0) ++n_act;
+      if (in && hf == 0 && p.lse) p.lse[row] = lse;
+      g += it;
+      if (it > 0) ++n_act;
     }
     if (!ok) *sAbort = 1;
     if (lane == 0) bulk_wait();
@@ -954,19 +928,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// rows of 128 channels in 64-channel boxes of box_rows rows, 128-byte swizzle
-bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
+// rows of 128 channels in boxes of box_rows rows x 64 channels (32 in the output's map), swizzled by the box's width
+bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_cols = 64) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
-  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t box[2] = {box_cols, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -989,7 +964,7 @@ cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
   const uint64_t pool_rows = static_cast<uint64_t>(p.n_pages) * p.page_size;
   const uint64_t ring_rows = static_cast<uint64_t>(p.n_seqs_layer) * p.n_win;
   const uint64_t chunk_rows = static_cast<uint64_t>(p.chunk_len);
-  if (!encode_rows(&tm_q, p.q, rows, kTileRows) || !encode_rows(&tm_out, p.out, rows, 32) ||
+  if (!encode_rows(&tm_q, p.q, rows, kTileRows) || !encode_rows(&tm_out, p.out, rows, 32, 32) ||
       !encode_rows(&tm_pool, p.kv_pool, pool_rows, 1) || !encode_rows(&tm_pool16, p.kv_pool, pool_rows, 16) ||
       !encode_rows(&tm_ring, p.ring_x, ring_rows, 1) || !encode_rows(&tm_ring16, p.ring_x, ring_rows, 16) ||
       !encode_rows(&tm_chunk, p.x_chunk, chunk_rows, 1) || !encode_rows(&tm_chunk16, p.x_chunk, chunk_rows, 16))
@@ -1000,7 +975,7 @@ cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = (rows + kItemRows - 1) / kItemRows;
   return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q,
-                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, tm_out, p);
+                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, tm_out, p, make_rule(p));
 }
 
 }  // namespace cskv
