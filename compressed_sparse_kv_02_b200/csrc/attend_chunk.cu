@@ -15,12 +15,11 @@
 // one's softmax runs, the other's P V and next S do.
 //   warps 0-15: softmax, two threads per row: warps 8 w + 4 h .. + 3 take keys
 //     64 h .. + 63 of tile w. (One thread per row, with two softmax warps on a
-//     scheduler, waited for its own instructions most of the time: 198.9 us where
-//     this takes NEW us.) The two agree on the row's reference maximum at a barrier,
-//     which moves only when a logit exceeds it by more than 2^8; O is rescaled
-//     then, half of its channels by each. O goes out through shared memory and TMA
-//     (written by the threads, 32 rows per instruction, it took 8,700 cycles per
-//     item);
+//     scheduler, waited for its own instructions most of the time: 198 us where two
+//     take 181.) With a running maximum the two agree on the row's reference at a
+//     barrier, and it moves only when a logit exceeds it by more than 2^8; O is
+//     rescaled then, half of its channels by each. O goes out a 32-byte sector per
+//     thread and store;
 //   warp 16: issues the MMAs;
 //   warps 17, 18: look up the keys' rows, four keys per lane, and have TMA copy the
 //     two 64-channel halves of each tile: 16 consecutive rows per copy where a run
@@ -35,7 +34,7 @@
 // half a reciprocal, which two tanh share): 3840 and 3072 cycles a pair; without it
 // 3 and 1, 770 and 2048.
 //
-// A row's segment is the run of consecutive queries of one sequence it stands in
+// Warp 19 describes the items. A row's segment is the run of consecutive queries of one sequence it stands in
 // (positions at most kMaxStep apart, so that a segment's windows overlap): the key
 // list of a segment is its queries' window positions wlo .. thi, padded to a
 // multiple of four, then the entries visible at thi, and each row's mask keeps its
@@ -61,30 +60,14 @@ constexpr int kNS = 3;                       // key stages
 constexpr int kHalfBytes = kNk * 128;        // 16384: one 64-channel half of 128 rows
 constexpr int kStageBytes = 2 * kHalfBytes;  // 32768 (also one Q tile)
 constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kLoadWarp0 = 17;
+constexpr int kMmaWarp = 16, kLoadWarp0 = 17;  // warp 19 describes the items
 constexpr int kTileThreads = 256;            // softmax threads of one tile
 constexpr int kMaxStep = 32;                 // largest step between positions of one segment's queries
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w (P over its first 64 columns), O at 256 + 128 w
+constexpr uint32_t kColS = 0, kColO = 256;   // S of tile w at 128 w (P of each 64 keys over theirs), O at 256 + 128 w
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;    // log2 units
-
-struct Smem {
-  static constexpr int Q = 0;
-  static constexpr int K = Q + 2 * kStageBytes;
-  static constexpr int OUT = K + kNS * kStageBytes;   // 32 channels of each softmax warp's rows on their way to TMA
-  static constexpr int POS = OUT + 2 * kHalfBytes;    // [kNS][kNk] key positions relative to the segment's last query
-  static constexpr int ROWS = POS + kNS * kNk * 4;    // [2][kNk] source-row codes (a tile copied by cp.async)
-  static constexpr int MASK = ROWS + 2 * kNk * 4;         // [kNS][4] valid-key bits
-  static constexpr int SIDE = MASK + kNS * 16;        // [2 tiles][2 halves][128 rows] maxima and sums the halves exchange
-  static constexpr int BAR = SIDE + 4 * kTileRows * 4;
-  static constexpr int TMEM = BAR + 24 * 8;
-  static constexpr int FLAGS = TMEM + 8;
-  static constexpr int END = FLAGS + 8;
-  static constexpr size_t bytes() { return 1024 + END; }
-};
-static_assert(Smem::bytes() <= 232448, "shared memory budget");
 
 // source-row code: kind in bits [31:30] (0 none, 1 pool entry, 2 ring row, 3 chunk row), row below
 constexpr uint32_t kRowBits = 30;
@@ -116,71 +99,79 @@ __device__ __forceinline__ int visible32(const AttendParams& p, int t, int lm) {
 }
 __device__ __forceinline__ int start32(const AttendParams& p, int t) { return max(t - p.n_win + 1, 0); }
 
-// The queries of an item (at most 17: 16 heads or more, rows that need not begin with a query), one per lane:
-// position (-1: no keys) and sequence.
-struct Queries {
-  int q0;           // first query
-  int t, seq;       // this lane's
-  unsigned starts;  // lanes where a segment begins
-  unsigned runs;    // lanes that belong to one
+// An item as one warp describes it to the others: its queries (at most 17: 16 heads or more, rows that need
+// not begin with a query) and its segments. The other roles keep a few numbers of it in registers at a time, which
+// leaves a softmax thread room for its 64 logits.
+struct Segment {
+  int s, e;         // queries s .. e - 1 of the item
+  int n_w, ntiles;  // window places of the key list, key tiles
+  int wlo, thi;     // its window positions
+  int seq, n;       // sequence, keys of the list
 };
-// this lane's query of an item, read one item ahead of its use
-struct RawQuery {
-  int64_t t;
-  int seq;
+struct ItemDesc {
+  int row0;  // first row (-1: no more items)
+  int h0;    // its head
+  int nseg, ntot;
+  int t[20];  // each query's position, -1 without keys
+  Segment seg[17];
 };
-__device__ __forceinline__ RawQuery fetch_query(const AttendParams& p, int item, int lane) {
-  RawQuery r = {-1, -1};
-  const int rows = p.n_q * p.n_heads;
-  const int64_t first = (int64_t)item * kItemRows;
-  if (first < rows) {
-    const int a = static_cast<int>(first), q = a / p.n_heads + lane;
-    if (q <= (min(a + kItemRows, rows) - 1) / p.n_heads) {
-      r.t = p.q_pos[q];
-      r.seq = p.q_seq[q];
-    }
+constexpr int kItems = 4;  // descriptors in flight
+static_assert(sizeof(ItemDesc) % 16 == 0 && sizeof(Segment) == 32, "descriptor layout");
+
+// Describes the item whose first row is `row0` = head h0 of query q0, one query per lane.
+__device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int row0, int q0, int h0, int rows, int lm,
+                                         int lane) {
+  int t = -1, seq = -1;
+  if (lane * p.n_heads < min(kItemRows, rows - row0) + h0) {
+    const int64_t pos = p.q_pos[q0 + lane];
+    seq = p.q_seq[q0 + lane];
+    if (pos >= 0 && pos <= p.max_pos && seq >= 0 && seq < p.n_seqs_layer) t = static_cast<int>(pos);
   }
-  return r;
-}
-__device__ __forceinline__ Queries item_queries(const AttendParams& p, int item, RawQuery raw, int lane) {
-  Queries r;
-  r.q0 = item * kItemRows / p.n_heads;
-  const bool ok = raw.t >= 0 && raw.t <= p.max_pos && raw.seq >= 0 && raw.seq < p.n_seqs_layer;
-  r.t = ok ? static_cast<int>(raw.t) : -1;
-  r.seq = raw.seq;
-  const int tp = __shfl_up_sync(kFull, r.t, 1);
-  const int sp = __shfl_up_sync(kFull, r.seq, 1);
-  const bool cont = lane > 0 && tp >= 0 && sp == r.seq && abs(r.t - tp) <= kMaxStep;
-  r.starts = __ballot_sync(kFull, ok && !cont);
-  r.runs = __ballot_sync(kFull, ok);
-  return r;
+  const int tp = __shfl_up_sync(kFull, t, 1);
+  const int sp = __shfl_up_sync(kFull, seq, 1);
+  const bool cont = lane > 0 && tp >= 0 && sp == seq && abs(t - tp) <= kMaxStep;
+  const unsigned starts = __ballot_sync(kFull, t >= 0 && !cont), runs = __ballot_sync(kFull, t >= 0);
+  if (lane < 20) d.t[lane] = t;
+  int ntot = 0, i = 0;
+  for (unsigned m = starts; m; m &= m - 1, ++i) {
+    Segment g;
+    g.s = __ffs(m) - 1;
+    const unsigned stop = (starts | ~runs) & ~((2u << g.s) - 1u);  // the first lane past s that begins another or none
+    g.e = stop ? __ffs(stop) - 1 : 32;
+    g.seq = __shfl_sync(kFull, seq, g.s);
+    const int ts = __shfl_sync(kFull, t, g.s);
+    const int mine = lane >= g.s && lane < g.e ? t : ts;
+    g.thi = __reduce_max_sync(kFull, mine);
+    g.wlo = start32(p, __reduce_min_sync(kFull, mine));
+    g.n_w = (g.thi - g.wlo + 4) & ~3;
+    g.n = g.n_w + visible32(p, g.thi, lm);
+    g.ntiles = (g.n + kNk - 1) / kNk;
+    ntot += g.ntiles;
+    if (lane == 0) d.seg[i] = g;
+  }
+  if (lane == 0) {
+    d.row0 = row0;
+    d.h0 = h0;
+    d.nseg = i;
+    d.ntot = ntot;
+  }
 }
 
-// One segment: lanes s .. e - 1, its key list (window positions wlo .. thi in n_w places, then entries, n in all).
-struct Segment {
-  int s, e, seq, n_w, n, ntiles, wlo, thi;
+struct Smem {
+  static constexpr int Q = 0;
+  static constexpr int K = Q + 2 * kStageBytes;
+  static constexpr int POS = K + kNS * kStageBytes;   // [kNS][kNk] key positions relative to the segment's last query
+  static constexpr int ROWS = POS + kNS * kNk * 4;    // [2][kNk] source-row codes (a tile copied by cp.async)
+  static constexpr int MASK = ROWS + 2 * kNk * 4;         // [kNS][4] valid-key bits
+  static constexpr int SIDE = MASK + kNS * 16;        // [2 tiles][2 halves][128 rows] maxima and sums the halves exchange
+  static constexpr int ITEM = SIDE + 4 * kTileRows * 4;  // [kItems] item descriptors
+  static constexpr int BAR = ITEM + kItems * sizeof(ItemDesc);
+  static constexpr int TMEM = BAR + 32 * 8;
+  static constexpr int FLAGS = TMEM + 8;
+  static constexpr int END = FLAGS + 8;
+  static constexpr size_t bytes() { return 1024 + END; }
 };
-__device__ __forceinline__ Segment segment_at(const AttendParams& p, const Queries& q, int s, int lane, int lm) {
-  Segment g;
-  g.s = s;
-  const unsigned after = ~((2u << s) - 1u);  // lanes past s
-  const unsigned stop = (q.starts | ~q.runs) & after;
-  g.e = stop ? __ffs(stop) - 1 : 32;
-  g.seq = __shfl_sync(kFull, q.seq, s);
-  const int ts = __shfl_sync(kFull, q.t, s);
-  const int t = lane >= s && lane < g.e ? q.t : ts;
-  g.thi = __reduce_max_sync(kFull, t);
-  g.wlo = start32(p, __reduce_min_sync(kFull, t));
-  g.n_w = (g.thi - g.wlo + 4) & ~3;
-  g.n = g.n_w + visible32(p, g.thi, lm);
-  g.ntiles = (g.n + kNk - 1) / kNk;
-  return g;
-}
-__device__ __forceinline__ int item_tiles(const AttendParams& p, const Queries& q, int lane, int lm) {
-  int n = 0;
-  for (unsigned m = q.starts; m; m &= m - 1) n += segment_at(p, q, __ffs(m) - 1, lane, lm).ntiles;
-  return n;
-}
+static_assert(Smem::bytes() <= 232448, "shared memory budget");
 
 // bits of lo <= u < hi for the 32 keys u = a .. a + 31
 __device__ __forceinline__ uint32_t range_bits(int a, int lo, int hi) {
@@ -230,16 +221,12 @@ __device__ __forceinline__ void commit_if(uint32_t issue, uint64_t* bar) {
       : "memory");
 }
 
-// 2D tiled TMA store from shared memory, and its bulk-group bookkeeping (per issuing thread)
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(smem_u32(src))
+// 32 bytes, a whole sector per thread
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;\n" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -285,14 +272,21 @@ Rule make_rule(const AttendParams& p) {
   return r;
 }
 
-// The rule on 64 logits, two packed pairs in step: with the cap, without, or capped below lim. bias = slope2 * position
+// The three forms of the kernel. kBounded: a cap of at most kMaxStatic (in log2 units) bounds every logit of a row to
+// [ref - cap2, ref + cap2] around a reference known beforehand, and the row's own token, or with a negative slope its
+// farthest key, reaches into that range, so 2^(s - ref) neither overflows fp32 nor vanishes, and the softmax needs no
+// running maximum: no pass for it, no agreement between the halves of a row, no rescaling (181 us -> STATIC us).
+enum Mode { kPlainMax, kCappedMax, kBounded };
+constexpr float kMaxStatic = 80.f;
+
+// The rule on N logits, two packed pairs in step: with the cap, without, or capped below lim. bias = slope2 * position
 // - ref, ref the row's running maximum so far (its subtraction costs nothing here).
 enum { kLinear, kRational, kPoly };
-template <int FORM>
-__device__ __forceinline__ void rule64(uint32_t (&s)[64], const float4* pos, const Rule& r, float2 slope,
+template <int FORM, int N>
+__device__ __forceinline__ void rule_n(uint32_t (&s)[N], const float4* pos, const Rule& r, float2 slope,
                                        float2 negref) {
 #pragma unroll
-  for (int b = 0; b < 64; b += 4) {
+  for (int b = 0; b < N; b += 4) {
     const float4 pa = pos[b / 4];
     float2 u[2] = {make_float2(__uint_as_float(s[b]), __uint_as_float(s[b + 1])),
                    make_float2(__uint_as_float(s[b + 2]), __uint_as_float(s[b + 3]))};
@@ -407,18 +401,18 @@ __device__ __noinline__ void slow_row(const AttendParams& p, int64_t row, float 
 //             wait pfull1 -> P V 1(g) -> kempty, S1(g + 1) -> sfull1 (or odone1); the last S1 of an item -> qempty
 //   softmax : wait sfull (S here, and every earlier P V of this tile done: O may be rescaled) -> P -> pfull;
 //             after the item's last tile: wait odone -> read O -> oread, which the next item's first P V waits for
-template <bool CAP>
+template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_pool,
                         const __grid_constant__ CUtensorMap tm_ring, const __grid_constant__ CUtensorMap tm_chunk,
                         const __grid_constant__ CUtensorMap tm_pool16, const __grid_constant__ CUtensorMap tm_ring16,
-                        const __grid_constant__ CUtensorMap tm_chunk16, const __grid_constant__ CUtensorMap tm_out,
+                        const __grid_constant__ CUtensorMap tm_chunk16,
                         const __grid_constant__ AttendParams p, const __grid_constant__ Rule r) {
+  constexpr bool CAP = MODE != kPlainMax;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Smem::Q;
   uint8_t* sK = sm + Smem::K;
-  uint8_t* sO = sm + Smem::OUT;
   float* sPos = reinterpret_cast<float*>(sm + Smem::POS);
   uint32_t* sRow = reinterpret_cast<uint32_t*>(sm + Smem::ROWS);
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
@@ -431,6 +425,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* oread = odone + 2;                                    // [2] softmax (8 warps) -> MMA
   uint64_t* qfull = oread + 2;                                    // [2] Q of the tile landed (TMA)
   uint64_t* qempty = qfull + 2;                                   // [2] the item's S products of the tile are done
+  uint64_t* ifull = qempty + 2;                                   // [kItems] descriptor written -> everyone
+  uint64_t* ifree = ifull + kItems;                               // [kItems] everyone (19 warps) -> item warp
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
 
@@ -440,6 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kNS; ++i) {
       mbar_init(&kfull[i], 2);
       mbar_init(&kempty[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&ifull[i], 1);
+      mbar_init(&ifree[i], 19);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
@@ -456,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_pool16);
     prefetch_tensormap(&tm_chunk16);
-    prefetch_tensormap(&tm_out);
   }
   if (warp == kMmaWarp) {
     tmem_alloc(sTmem, kTmemCols);
@@ -477,8 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         report(p.status, CSKV_ERR_OUT_OF_RANGE);
     }
   const int rows = p.n_q * p.n_heads;
-  const int n_items = (rows + kItemRows - 1) / kItemRows;
   const int lm = __ffs(p.m) - 1;  // m is a power of two
+  ItemDesc* items = reinterpret_cast<ItemDesc*>(sm + Smem::ITEM);
+  uint32_t n_item = 0;  // items before the current one
+  // the current item's descriptor, and giving it back (whole warps)
+  auto item_wait = [&](uint32_t n) {
+    return __all_sync(kFull, mbar_wait(&ifull[n % kItems], (n / kItems) & 1u, p.status));
+  };
+  auto item_done = [&](uint32_t n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ifree[n % kItems]);
+  };
   uint32_t g = 0;      // key tiles before the current item
   uint32_t n_act = 0;  // items with keys before the current one
 
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t v = sKa + st * kStageBytes;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          umma_ts_if(issuer, tmem + kColO + w * kD, tmem + kColS + w * kNk + ks * 8,
+          umma_ts_if(issuer, tmem + kColO + w * kD, tmem + kColS + w * kNk + (ks >> 2) * 64 + (ks & 3) * 8,
                      umma_desc_sw128(v + ks * 16 * 128, kHalfBytes, 1024), idesc_pv, ks > 0 ? 1u : acc);
       };
       // the stage as a constant in each branch, so that the descriptors are
@@ -524,20 +532,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       static_assert(kNS == 3, "the stage branches");
       // the items with keys, found one ahead: S of the next item's first key tile is issued behind P V of this
       // item's last one, so the softmax of a tile goes from item to item without a pause
-      int item = blockIdx.x;
-      RawQuery raw = fetch_query(p, item, lane);
+      bool ok = true;
       auto next_tiles = [&]() {  // key tiles of the next item that has any, 0 at the end
-        for (; item < n_items;) {
-          const int n = __shfl_sync(kFull, item_tiles(p, item_queries(p, item, raw, lane), lane, lm), 0);
-          item += gridDim.x;
-          raw = fetch_query(p, item, lane);
+        while (ok) {
+          if (!(ok = item_wait(n_item))) break;
+          const ItemDesc& d = items[n_item % kItems];
+          const int row0 = __shfl_sync(kFull, d.row0, 0), n = __shfl_sync(kFull, d.ntot, 0);
+          item_done(n_item++);
+          if (row0 < 0) {
+            --n_item;  // the end stays where it is
+            return 0;
+          }
           if (n) return n;
         }
         return 0;
       };
       int ntot = next_tiles();
-      bool ok = true;
-      if (ntot) {
+      if (ntot && ok) {
         for (int w = 0; w < 2 && ok; ++w) {
           ok = wait(&qfull[w], 0) && wait(&kfull[0], 0);
           if (!ok) break;
@@ -548,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       while (ntot && ok) {
         const int nnext = next_tiles();
+        if (!ok) break;
         for (int it = 0; it < ntot && ok; ++it) {
           if (__shfl_sync(kFull, *sAbort, 0)) {
             ok = false;
@@ -591,26 +603,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int half = warp - kLoadWarp0;
       bool ok = true;
       uint32_t issued = 0, q_issued = 0;  // key tiles and Q loads given to TMA
-      RawQuery raw = fetch_query(p, blockIdx.x, lane);
-      for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-        const Queries q = item_queries(p, item, raw, lane);
-        raw = fetch_query(p, item + gridDim.x, lane);
-        const int ntot = item_tiles(p, q, lane, lm);
-        if (ntot == 0) continue;
-        // Q of a tile once the last item's S products are done with it
+      for (; ok; ++n_item) {
+        if (!(ok = item_wait(n_item))) break;
+        const ItemDesc& d = items[n_item % kItems];
+        const int row0 = d.row0, ntot = d.ntot;
+        if (row0 < 0) break;
+        if (ntot == 0) {
+          item_done(n_item);
+          continue;
+        }
         ok = __all_sync(kFull, n_act == 0 || mbar_wait(&qempty[half], (n_act - 1) & 1u, p.status));
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&qfull[half], kStageBytes);
           for (int h = 0; h < 2; ++h)
-            tma_load_2d(sQ + half * kStageBytes + h * kHalfBytes, &tm_q, h * 64, item * kItemRows + half * kTileRows,
+            tma_load_2d(sQ + half * kStageBytes + h * kHalfBytes, &tm_q, h * 64, row0 + half * kTileRows,
                         &qfull[half]);
         }
         __syncwarp();
         ++q_issued;
         uint32_t gt = g;
-        for (unsigned ms = q.starts; ms && ok; ms &= ms - 1) {
-          const Segment sg = segment_at(p, q, __ffs(ms) - 1, lane, lm);
+        for (int i = 0; i < d.nseg && ok; ++i) {
+          const Segment sg = d.seg[i];
           for (int it = 0; it < sg.ntiles; ++it, ++gt) {
             const int st = gt % kNS;
             // keys u .. u + 3 of the list: all window places, or all entries (of one page)
@@ -697,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             issued = gt + 1;
           }
         }
+        item_done(n_item);
         g += ntot;
         ++n_act;
       }
@@ -707,6 +722,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q_issued > 0) mbar_wait(&qfull[half], (q_issued - 1) & 1u, nullptr);
       }
     }
+    else {
+      // ---------------------------------------------------------------- items
+      int row0 = blockIdx.x * kItemRows, q0 = row0 / p.n_heads, h0 = row0 % p.n_heads;
+      const int step = gridDim.x * kItemRows, dq = step / p.n_heads, dh = step % p.n_heads;
+      bool ok = true;
+      for (; ok; ++n_item) {
+        ok = __all_sync(kFull, n_item < kItems || mbar_wait(&ifree[n_item % kItems], ((n_item / kItems) - 1) & 1u, p.status));
+        if (!ok) break;
+        ItemDesc& d = items[n_item % kItems];
+        if (row0 < rows)
+          describe(p, d, row0, q0, h0, rows, lm, lane);
+        else if (lane == 0)
+          d.row0 = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ifull[n_item % kItems]);
+        if (row0 >= rows) break;
+        row0 += step;
+        q0 += dq;
+        h0 += dh;
+        if (h0 >= p.n_heads) {
+          h0 -= p.n_heads;
+          ++q0;
+        }
+      }
+      if (!ok) *sAbort = 1;
+    }
   } else {
     // ------------------------------------------------------------------ softmax (half a row per thread)
     // Every softmax warp of a tile reaches the tile's barriers; a bounded wait that gave up only marks the tile bad,
@@ -714,36 +755,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
     const int w = warp >> 3, hf = (warp >> 2) & 1, tr = (warp & 3) * 32 + lane;  // tile, key half, row of the tile
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // S of my keys; P of a tile lies over the first half of its S; O of my channels
-    const uint32_t sb = trow + kColS + w * kNk + 64 * hf, pb = trow + kColS + w * kNk + 32 * hf;
+    // S of my keys (their P goes over its first 32 columns), O of my channels
+    const uint32_t sb = trow + kColS + w * kNk + 64 * hf;
     const uint32_t ob = trow + kColO + w * kD + 64 * hf;
     float* side = sSide + (2 * w + hf) * kTileRows + tr;
     float* other = sSide + (2 * w + (hf ^ 1)) * kTileRows + tr;
-    uint8_t* obuf = sO + warp * 2048;  // this warp's 32 rows of 32 channels
+    const float inv_heads = 1.f / static_cast<float>(p.n_heads);
     bool ok = true;
-    RawQuery raw = fetch_query(p, blockIdx.x, lane);
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const Queries q = item_queries(p, item, raw, lane);
-      raw = fetch_query(p, item + gridDim.x, lane);
-      const int row = item * kItemRows + w * kTileRows + tr;
+    for (; ok; ++n_item) {
+      if (named_sync_or(1 + w, kTileThreads, !item_wait(n_item))) {
+        ok = false;
+        break;
+      }
+      const ItemDesc& d = items[n_item % kItems];
+      const int row = d.row0 + w * kTileRows + tr;
+      if (d.row0 < 0) break;
       const bool in = row < rows;
-      const int qi = in ? row / p.n_heads - q.q0 : 0;  // this row's query lane
-      const int t = __shfl_sync(kFull, q.t, qi);
-      const float slope2 = p.slopes && in ? p.slopes[row % p.n_heads] * kLog2e : 0.f;
+      // this row's query within the item and its head: small whole numbers, so the rounded quotient is exact
+      const int at = d.h0 + w * kTileRows + tr;
+      const int qi = static_cast<int>((static_cast<float>(at) + 0.5f) * inv_heads);
+      const float slope2 = p.slopes && in ? p.slopes[at - qi * p.n_heads] * kLog2e : 0.f;
+      const int t = in ? d.t[qi] : -1;
       float m_used = -INFINITY, l_run = 0.f;
       int shift = 0;  // the row's logits are taken at distance 0 of its segment's last query
       int it = 0;
-      for (unsigned ms = q.starts; ms && ok; ms &= ms - 1) {
-        const Segment sg = segment_at(p, q, __ffs(ms) - 1, lane, lm);
+      bool fail = false;  // kBounded: a wait gave up (the item's barrier tells the others)
+      float2 l_a = make_float2(0.f, 0.f), l_b = l_a;
+      // kBounded: the reference, 0 where near keys lead and the farthest key's bias where far ones do
+      float ref = 0.f;
+      if (MODE == kBounded && slope2 < 0.f && t >= 0)
+        ref = -slope2 * (visible32(p, t, lm) > 0 ? entry_distance(t, 0, p.m) : static_cast<float>(t - start32(p, t)));
+      for (int i = 0; i < d.nseg && ok && !fail; ++i) {
+        const Segment& sg = d.seg[i];
         // this row's keys in the segment's list: window lo .. hi - 1, entries n_w .. end - 1
+        const int n_w = sg.n_w, ntiles = sg.ntiles;
         int lo = 0, hi = 0, end = 0;
-        if (in && t >= 0 && qi >= sg.s && qi < sg.e) {
+        if (t >= 0 && qi >= sg.s && qi < sg.e) {
           lo = start32(p, t) - sg.wlo;
           hi = t - sg.wlo + 1;
-          end = sg.n_w + visible32(p, t, lm);
+          end = n_w + visible32(p, t, lm);
           shift = t - sg.thi;
         }
-        for (int k = 0; k < sg.ntiles; ++k, ++it) {
+        for (int k = 0; k < ntiles; ++k, ++it) {
           const uint32_t gt = g + it;
           const int st = gt % kNS;
           // the stage's positions and key bits were written before kfull; that phase cannot move on before this
@@ -751,6 +804,55 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool good = __all_sync(kFull, mbar_wait(&sfull[w], gt & 1u, p.status)) &&
                       __all_sync(kFull, mbar_wait(&kfull[st], (gt / kNS) & 1u, p.status));
           tc_fence_after();
+          if constexpr (MODE == kBounded) {
+            if (!good) {
+              fail = true;
+              break;
+            }
+            uint32_t sa[32], sc[32];
+            tmem_ld32(sb, sa);
+            tmem_ld_wait();
+            tmem_ld32(sb + 32, sc);
+            const float nr = -slope2 * static_cast<float>(shift) - ref;
+            const float2 negref = make_float2(nr, nr), sl = make_float2(slope2, slope2);
+            const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf);
+            auto part = [&](int c, uint32_t (&s)[32]) {
+              float big = 0.f, big1 = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                big = max3_abs(big, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+              }
+              if (__all_sync(kFull, fmaxf(big, big1) <= r.lim))
+                rule_n<kPoly>(s, pos4 + 8 * c, r, sl, negref);
+              else
+                rule_n<kRational>(s, pos4 + 8 * c, r, sl, negref);
+              const int a = k * kNk + 64 * hf + 32 * c;
+              const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, n_w, end));
+              if (__any_sync(kFull, vm != kFull)) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!((vm >> j) & 1u)) s[j] = 0xff800000u;  // -inf
+              }
+              uint32_t pp[16];
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float2 e = make_float2(ex2(__uint_as_float(s[2 * j])), ex2(__uint_as_float(s[2 * j + 1])));
+                if (j & 1) l_b = __fadd2_rn(l_b, e);
+                else l_a = __fadd2_rn(l_a, e);
+                pp[j] = pack_bf16(e.x, e.y);
+              }
+              tmem_st16(sb + 16 * c, pp);
+            };
+            part(0, sa);
+            tmem_ld_wait();
+            part(1, sc);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[w]);
+            continue;
+          }
           uint32_t s[64];
           tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
           tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
@@ -767,18 +869,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
               }
               if (__all_sync(kFull, fmaxf(big, big1) <= r.lim))
-                rule64<kPoly>(s, pos4, r, sl, negref);
+                rule_n<kPoly>(s, pos4, r, sl, negref);
               else
-                rule64<kRational>(s, pos4, r, sl, negref);
+                rule_n<kRational>(s, pos4, r, sl, negref);
             } else {
-              rule64<kLinear>(s, pos4, r, sl, negref);
+              rule_n<kLinear>(s, pos4, r, sl, negref);
             }
           }
           float mt = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const int a = k * kNk + 64 * hf + 32 * c;
-            const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, sg.n_w, end));
+            const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, n_w, end));
             if (__any_sync(kFull, vm != kFull)) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
@@ -792,8 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mt = max3(mt, m0, m1);
           }
-          // The logits stand on the old maximum (0 before the row's first key). Both halves of the tile's rows have
-          // read S once they meet here, so P may be written over it.
+          // The logits stand on the old maximum (0 before the row's first key).
           const bool fresh = m_used == -INFINITY;
           const bool bad = !good || *sAbort != 0;
           if (named_sync_or(1 + w, kTileThreads, bad || mt > kRescaleThreshold || (fresh && mt != -INFINITY))) {
@@ -833,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               else la = __fadd2_rn(la, make_float2(e0, e1));
               pp[j] = pack_bf16(e0, e1);
             }
-            tmem_st16(pb + 16 * c, pp);
+            tmem_st16(sb + 16 * c, pp);
           }
           la = __fadd2_rn(la, lb);
           l_run += la.x + la.y;
@@ -845,53 +946,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // epilogue: O / l in bf16 (64 channels per thread), and the log-sum-exp
+      if constexpr (MODE == kBounded) {
+        l_a = __fadd2_rn(l_a, l_b);
+        l_run = l_a.x + l_a.y;
+        m_used = ref;
+        shift = 0;
+      }
       *side = l_run;
-      const bool done = it == 0 || __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status));
+      const bool done = it == 0 || fail || __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status));
       tc_fence_after();
-      if (named_sync_or(1 + w, kTileThreads, !done)) {
+      if (named_sync_or(1 + w, kTileThreads, !done || fail)) {
         ok = false;
         break;
       }
       l_run += *other;
       const bool has = in && l_run > 0.f;
       const float inv = has ? 1.f / l_run : 0.f;
-      const int first = row - lane;  // of this warp's rows
-      float odd = 0.f;               // NaN once an output is not finite
+      float odd = 0.f;  // NaN once an output is not finite
 #pragma unroll 1
-      for (int c = 0; c < 64; c += 32) {
-        if (lane == 0) bulk_wait_read();  // TMA has read what the buffer held
-        __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          uint32_t o[16];
-          if (it > 0) {
-            tmem_ld16(ob + c + 16 * i, o);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            o[e] = has ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-            odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
-          }
-          // inverse RoPE of the output's last rope_dims channels
-          if (p.rope_dims > 0 && has) rope16(o, 64 * hf + c + 16 * i, p, t);
-          // 64-byte rows, 16-byte pieces swizzled by address bits 7 and 8
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t v[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v[j] = pack_bf16(__uint_as_float(o[8 * e + 2 * j]), __uint_as_float(o[8 * e + 2 * j + 1]));
-            *reinterpret_cast<uint4*>(obuf + lane * 64 + (((2 * i + e) ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
-          }
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t o[16], v[8];
+        if (it > 0) {
+          tmem_ld16(ob + c, o);
+          tmem_ld_wait();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && first < rows) {  // rows past the last one are not written
-          tma_store_2d(&tm_out, 64 * hf + c, first, obuf);
-          bulk_commit();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          o[e] = has ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+          odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
         }
+        if (p.rope_dims > 0 && has) rope16(o, 64 * hf + c, p, t);  // the output's last rope_dims channels
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+        if (in) store32(p.out + (int64_t)row * kD + 64 * hf + c, v);
       }
       // the next item's first P V overwrites O: this warp's reads of it are complete
       tc_fence_before();
@@ -899,8 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it > 0 && lane == 0) mbar_arrive(&oread[w]);
       float lse = has ? (m_used + log2f(l_run) - slope2 * static_cast<float>(shift)) * kLn2 : -INFINITY;
       const unsigned redo = __ballot_sync(kFull, in && (l_run != l_run || !(odd == 0.f)));
-      if (redo) {  // rows to take again (my channels of them): TMA's stores of them are done first
-        if (lane == 0) bulk_wait();
+      if (redo) {  // rows to take again, my channels of them, over what their threads stored
         __syncwarp();
         for (unsigned left = redo; left; left &= left - 1) {
           const int b = __ffs(left) - 1;  // one row at a time, by the whole warp
@@ -918,11 +1004,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (in && hf == 0 && p.lse) p.lse[row] = lse;
+      item_done(n_item);
       g += it;
       if (it > 0) ++n_act;
     }
     if (!ok) *sAbort = 1;
-    if (lane == 0) bulk_wait();
   }
   cp_async_wait<0>();
   tc_fence_before();
@@ -931,17 +1017,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// rows of 128 channels in boxes of box_rows rows x 64 channels (32 in the output's map), swizzled by the box's width
-bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows, uint32_t box_cols = 64) {
+// rows of 128 channels in 64-channel boxes of box_rows rows, 128-byte swizzle
+bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
-  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -953,29 +1038,30 @@ bool attend_chunk_supported(const AttendParams& p, int n_sm) {
   const uint64_t ring_rows = static_cast<uint64_t>(p.n_seqs_layer) * p.n_win;
   const int64_t rows = (int64_t)p.n_q * p.n_heads;
   return !p.is_csa && has_score_rule(p) && p.x_chunk && p.d_qk == kD && p.d_v == kD && p.n_heads >= 16 &&
-         p.kv_dtype == CSKV_BF16 && rows >= (int64_t)kItemRows * n_sm / 2 && rows <= 0x7fffffff - kItemRows &&
+         p.kv_dtype == CSKV_BF16 && rows >= (int64_t)kItemRows * n_sm / 2 && rows <= 0x7fffffff - (int64_t)kItemRows * (n_sm + 1) &&
          p.max_pos < (1 << 30) && p.n_win < (1 << 30) && p.chunk_len > 0 &&
          pool_rows <= kRowMask && ring_rows <= kRowMask && static_cast<uint64_t>(p.chunk_len) <= kRowMask;
 }
 
 cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
-  CUtensorMap tm_q, tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, tm_out;
+  CUtensorMap tm_q, tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16;
   const int64_t rows = (int64_t)p.n_q * p.n_heads;
   const uint64_t pool_rows = static_cast<uint64_t>(p.n_pages) * p.page_size;
   const uint64_t ring_rows = static_cast<uint64_t>(p.n_seqs_layer) * p.n_win;
   const uint64_t chunk_rows = static_cast<uint64_t>(p.chunk_len);
-  if (!encode_rows(&tm_q, p.q, rows, kTileRows) || !encode_rows(&tm_out, p.out, rows, 32, 32) ||
+  if (!encode_rows(&tm_q, p.q, rows, kTileRows) ||
       !encode_rows(&tm_pool, p.kv_pool, pool_rows, 1) || !encode_rows(&tm_pool16, p.kv_pool, pool_rows, 16) ||
       !encode_rows(&tm_ring, p.ring_x, ring_rows, 1) || !encode_rows(&tm_ring16, p.ring_x, ring_rows, 16) ||
       !encode_rows(&tm_chunk, p.x_chunk, chunk_rows, 1) || !encode_rows(&tm_chunk16, p.x_chunk, chunk_rows, 16))
     return cudaErrorNotSupported;
   const size_t smem = Smem::bytes();
-  auto kern = p.score_cap > 0.f ? attend_chunk_kernel<true> : attend_chunk_kernel<false>;
+  auto kern = p.score_cap <= 0.f ? attend_chunk_kernel<kPlainMax>
+              : p.score_cap * kLog2e <= kMaxStatic ? attend_chunk_kernel<kBounded> : attend_chunk_kernel<kCappedMax>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int64_t items = (rows + kItemRows - 1) / kItemRows;
   return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q,
-                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, tm_out, p, make_rule(p));
+                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, p, make_rule(p));
 }
 
 }  // namespace cskv

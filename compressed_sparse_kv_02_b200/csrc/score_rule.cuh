@@ -10,11 +10,11 @@ namespace cskv {
 // reweighted by the error), clamped there (1 - tanh(8) = 2.3e-7). The relative form keeps small arguments, so a
 // large cap leaves the logits as they are; 1 - 2 / (1 + e^2u) would lose cap * 2^-23 and take a second
 // special-function operation, which is what bounds the capped softmax (16 per clock and SM).
-__device__ constexpr float tanh_n(int i) {  // coefficients of N and D, constant term first
+__host__ __device__ constexpr float tanh_n(int i) {  // coefficients of N and D, constant term first
   return i == 0 ? 0.9999998807907104f : i == 1 ? 0.12925660610198975f : i == 2 ? 0.002951021073386073f
                                                                                : 1.1428394827817101e-05f;
 }
-__device__ constexpr float tanh_d(int i) {
+__host__ __device__ constexpr float tanh_d(int i) {
   return i == 0 ? 1.f : i == 1 ? 0.46258875727653503f : i == 2 ? 0.023815542459487915f
                       : i == 3 ? 0.00023866878473199904f : 2.4592020508862333e-07f;
 }

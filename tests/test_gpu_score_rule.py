@@ -157,7 +157,7 @@ class Setup:
                 assert bool((el <= D + 2.0 ** -20 * (l.abs() + 1)).all()), (i, float(el.max()), float(D.max()))
 
 
-RULES = [(30.0, True), (20.0, False), (0.0, True)]
+RULES = [(30.0, True), (20.0, False), (0.0, True), (70.0, True)]  # 70: above what bounds the chunk form's logits
 
 
 def _both(s, rules=RULES, queries=None):
@@ -250,7 +250,24 @@ def test_rule_off_and_extreme_caps(ck, kind, d_qk, d_v, H, n_q):
     s = Setup(ck, kind, d_qk, d_v, H, [0] * n_q, pos, k=64 if kind == "csa" else 0, seed=12, chunk={0: (0, 2000, n_q)})
     some = sorted({0, n_q // 2, n_q - 1})
     zero = torch.zeros_like(s.slopes)
-    for cap, slopes in ((0.0, zero), (1e30, None), (2.0 ** 100, zero), (1e-3, None), (0.0, -s.slopes / 64), (1e-30, None)):
+    for cap, slopes in ((0.0, zero), (1e30, None), (2.0 ** 100, zero), (1e-3, None), (0.0, -s.slopes / 64), (1e-30, None),
+                        (20.0, -s.slopes / 64), (55.0, s.slopes)):
+        out, lse = s.run(cap, slopes)
+        s.check(out, lse, cap, slopes, some)
+
+
+@pytest.mark.parametrize("cap", [20.0, 55.0, 70.0])
+def test_chunk_with_far_logits(ck, cap):
+    """Logits at the cap on both sides, rows whose keys all sit at the lower one, and biases that bury all but the
+    nearest keys: sums from 2^-80 to 2^80 around the reference."""
+    n, pos0, H = 700, 3000, 64
+    s = Setup(ck, "hca", 128, 128, H, [0] * n, list(range(pos0, pos0 + n)), seed=18, chunk={0: (0, pos0, n)}, q_std=40.0)
+    s.q[:, 1::4] = s.q[:, 1::4].abs()
+    s.x_chunk[: n // 2] = -s.x_chunk[: n // 2].abs()  # heads 1, 5, ..: every near key far below
+    steep = s.slopes.clone()
+    steep[::2] = 3.0
+    some = [0, 1, 127, 128, 200, 349, 350, 351, 480, 699]
+    for slopes in (None, steep, -s.slopes / 64):
         out, lse = s.run(cap, slopes)
         s.check(out, lse, cap, slopes, some)
 
