@@ -18,8 +18,7 @@
 //     scheduler, waited for its own instructions most of the time: 198 us where two
 //     take 181.) With a running maximum the two agree on the row's reference at a
 //     barrier, and it moves only when a logit exceeds it by more than 2^8; O is
-//     rescaled then, half of its channels by each. O goes out a 32-byte sector per
-//     thread and store;
+//     rescaled then, half of its channels by each;
 //   warp 16: issues the MMAs;
 //   warps 17, 18: look up the keys' rows, four keys per lane, and have TMA copy the
 //     two 64-channel halves of each tile: 16 consecutive rows per copy where a run
@@ -34,7 +33,11 @@
 // half a reciprocal, which two tanh share): 3840 and 3072 cycles a pair; without it
 // 3 and 1, 770 and 2048.
 //
-// Warp 19 describes the items. A row's segment is the run of consecutive queries of one sequence it stands in
+//   warp 19: describes the items;
+//   warps 20-23: write O / l, a row per thread and a 32-byte sector per store, while
+//     the softmax warps are at the next item (as a part of their work it took a
+//     third of an item's time).
+// A row's segment is the run of consecutive queries of one sequence it stands in
 // (positions at most kMaxStep apart, so that a segment's windows overlap): the key
 // list of a segment is its queries' window positions wlo .. thi, padded to a
 // multiple of four, then the entries visible at thi, and each row's mask keeps its
@@ -59,8 +62,8 @@ constexpr int kNk = 128;                     // keys per tile
 constexpr int kNS = 3;                       // key stages
 constexpr int kHalfBytes = kNk * 128;        // 16384: one 64-channel half of 128 rows
 constexpr int kStageBytes = 2 * kHalfBytes;  // 32768 (also one Q tile)
-constexpr int kThreads = 640;
-constexpr int kMmaWarp = 16, kLoadWarp0 = 17;  // warp 19 describes the items
+constexpr int kThreads = 768;
+constexpr int kMmaWarp = 16, kLoadWarp0 = 17, kItemWarp = 19;  // 20 .. 23 write the outputs
 constexpr int kTileThreads = 256;            // softmax threads of one tile
 constexpr int kMaxStep = 32;                 // largest step between positions of one segment's queries
 constexpr uint32_t kTmemCols = 512;
@@ -163,8 +166,10 @@ struct Smem {
   static constexpr int POS = K + kNS * kStageBytes;   // [kNS][kNk] key positions relative to the segment's last query
   static constexpr int ROWS = POS + kNS * kNk * 4;    // [2][kNk] source-row codes (a tile copied by cp.async)
   static constexpr int MASK = ROWS + 2 * kNk * 4;         // [kNS][4] valid-key bits
-  static constexpr int SIDE = MASK + kNS * 16;        // [2 tiles][2 halves][128 rows] maxima and sums the halves exchange
-  static constexpr int ITEM = SIDE + 4 * kTileRows * 4;  // [kItems] item descriptors
+  static constexpr int SIDE = MASK + kNS * 16;        // [2 tiles][2 halves][128 rows] maxima the halves exchange
+  static constexpr int SUM = SIDE + 4 * kTileRows * 4;   // [2 tiles][2 halves][128 rows] an item's sums
+  static constexpr int BASE = SUM + 4 * kTileRows * 4;  // [2 tiles][128 rows] what a row's sum stands on
+  static constexpr int ITEM = BASE + 2 * kTileRows * 4;  // [kItems] item descriptors
   static constexpr int BAR = ITEM + kItems * sizeof(ItemDesc);
   static constexpr int TMEM = BAR + 32 * 8;
   static constexpr int FLAGS = TMEM + 8;
@@ -345,22 +350,9 @@ __device__ __forceinline__ void rule_n(uint32_t (&s)[N], const float4* pos, cons
   }
 }
 
-// Inverse RoPE of 16 output channels ch0 .. ch0 + 15, out of the way of the registers of its caller
-__device__ __noinline__ void rope16(uint32_t (&o)[16], int ch0, const AttendParams& p, int t) {
-#pragma unroll 1
-  for (int i = 0; i < 16; i += 4) {
-    float f[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(o[i + e]);
-    inverse_rope4(f, ch0 + i, kD, p.rope_dims, p.rope_base, t);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i + e] = __float_as_uint(f[e]);
-  }
-}
-
 // One row from its own keys only, by one warp (lane = 4 channels): scores in fp32, an online softmax, fp32 P.
 template <bool CAP>
-__device__ __noinline__ void slow_row(const AttendParams& p, int64_t row, float sl2, float cap2, float slope2, float (&o)[4],
+__device__ __forceinline__ void slow_row(const AttendParams& p, int64_t row, float sl2, float cap2, float slope2, float (&o)[4],
                                       float& m, float& l, int lane) {
   const int b = static_cast<int>(row / p.n_heads);
   const int t = static_cast<int>(p.q_pos[b]), ws = start32(p, t);
@@ -400,7 +392,8 @@ __device__ __noinline__ void slow_row(const AttendParams& p, int64_t row, float 
 //   MMA     : S0(0) S1(0), then per key tile: wait pfull0 -> P V 0(g), S0(g + 1) -> sfull0 (or odone0);
 //             wait pfull1 -> P V 1(g) -> kempty, S1(g + 1) -> sfull1 (or odone1); the last S1 of an item -> qempty
 //   softmax : wait sfull (S here, and every earlier P V of this tile done: O may be rescaled) -> P -> pfull;
-//             after the item's last tile: wait odone -> read O -> oread, which the next item's first P V waits for
+//             after the item's last tile: its rows' sums -> lready
+//   outputs : wait lready, odone -> read O -> oread, which the next item's first P V waits for
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_pool,
@@ -417,16 +410,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* sRow = reinterpret_cast<uint32_t*>(sm + Smem::ROWS);
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
   float* sSide = reinterpret_cast<float*>(sm + Smem::SIDE);
+  float* sSum = reinterpret_cast<float*>(sm + Smem::SUM);
+  float* sBase = reinterpret_cast<float*>(sm + Smem::BASE);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + Smem::BAR);  // [3] loaders (2) -> MMA, softmax
   uint64_t* kempty = kfull + kNS;                                 // [3] MMA -> loaders
   uint64_t* sfull = kempty + kNS;                                 // [2] MMA -> softmax
   uint64_t* pfull = sfull + 2;                                    // [2] softmax (8 warps) -> MMA
-  uint64_t* odone = pfull + 2;                                    // [2] MMA -> softmax
-  uint64_t* oread = odone + 2;                                    // [2] softmax (8 warps) -> MMA
+  uint64_t* odone = pfull + 2;                                    // [2] MMA -> output warps
+  uint64_t* oread = odone + 2;                                    // [2] output warps (4) -> MMA
   uint64_t* qfull = oread + 2;                                    // [2] Q of the tile landed (TMA)
   uint64_t* qempty = qfull + 2;                                   // [2] the item's S products of the tile are done
-  uint64_t* ifull = qempty + 2;                                   // [kItems] descriptor written -> everyone
-  uint64_t* ifree = ifull + kItems;                               // [kItems] everyone (19 warps) -> item warp
+  uint64_t* lready = qempty + 2;                                  // [2] softmax (8 warps): an item's sums -> output warps
+  uint64_t* lfree = lready + 2;                                   // [2] output warps (4) have read them
+  uint64_t* ifull = lfree + 2;                                   // [kItems] descriptor written -> everyone
+  uint64_t* ifree = ifull + kItems;                               // [kItems] everyone (23 warps) -> item warp
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
 
@@ -439,13 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&ifull[i], 1);
-      mbar_init(&ifree[i], 19);
+      mbar_init(&ifree[i], 23);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 8);
       mbar_init(&odone[i], 1);
-      mbar_init(&oread[i], 8);
+      mbar_init(&oread[i], 4);
+      mbar_init(&lready[i], 8);
+      mbar_init(&lfree[i], 4);
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], 1);
     }
@@ -491,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t n_act = 0;  // items with keys before the current one
 
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issue (lane 0; the warp waits together)
       const uint32_t issuer = elect_one();
@@ -722,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q_issued > 0) mbar_wait(&qfull[half], (q_issued - 1) & 1u, nullptr);
       }
     }
-    else {
+    else if (warp == kItemWarp) {
       // ---------------------------------------------------------------- items
       int row0 = blockIdx.x * kItemRows, q0 = row0 / p.n_heads, h0 = row0 % p.n_heads;
       const int step = gridDim.x * kItemRows, dq = step / p.n_heads, dh = step % p.n_heads;
@@ -747,26 +746,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) *sAbort = 1;
+    } else {
+      // ---------------------------------------------------------------- outputs: O / l in bf16, and the log-sum-exp
+      const int tr = (warp & 3) * 32 + lane;  // row of the tile
+      const uint32_t otile = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO;
+      bool ok = true;
+      for (; ok; ++n_item) {
+        if (!(ok = item_wait(n_item))) break;
+        const ItemDesc& d = items[n_item % kItems];
+        if (d.row0 < 0) break;
+        const int ntot = d.ntot;
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          const int row = d.row0 + w * kTileRows + tr;
+          const bool in = row < rows;
+          ok = __all_sync(kFull, mbar_wait(&lready[w], n_item & 1u, p.status));
+          if (!ok) break;
+          const float l = sSum[2 * w * kTileRows + tr] + sSum[(2 * w + 1) * kTileRows + tr];
+          const float base = sBase[w * kTileRows + tr];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&lfree[w]);
+          if (ntot > 0 && !(ok = __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status)))) break;
+          tc_fence_after();
+          const bool has = in && l > 0.f;
+          const float inv = has ? 1.f / l : 0.f;
+          float odd = 0.f;  // NaN once an output is not finite
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16], v[8];
+            if (ntot > 0) {
+              tmem_ld16(otile + w * kD + c, o);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              o[e] = has ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
+              odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+            if (in) store32(p.out + (int64_t)row * kD + c, v);
+          }
+          // the next item's first P V overwrites O: this warp's reads of it are complete
+          tc_fence_before();
+          __syncwarp();
+          if (ntot > 0 && lane == 0) mbar_arrive(&oread[w]);
+          float lse = has ? (base + log2f(l)) * kLn2 : -INFINITY;
+          const unsigned redo = __ballot_sync(kFull, in && (l != l || !(odd == 0.f)));
+          if (redo) __syncwarp();
+          for (unsigned left = redo; left; left &= left - 1) {
+            const int b = __ffs(left) - 1;  // one row at a time, by the whole warp, over what its thread stored
+            const int rr = __shfl_sync(kFull, row, b);
+            const float slope2 = p.slopes ? p.slopes[rr % p.n_heads] * kLog2e : 0.f;
+            float o4[4], m, lr;
+            slow_row<CAP>(p, rr, r.pre.x, r.cap2.x, slope2, o4, m, lr, lane);
+            const float iv = 1.f / lr;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o4[e] *= iv;
+            *reinterpret_cast<uint2*>(p.out + (int64_t)rr * kD + 4 * lane) =
+                make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
+            if (lane == b) lse = (m + log2f(lr)) * kLn2;
+          }
+          if (in && p.lse) p.lse[row] = lse;
+        }
+        if (!ok) break;
+        item_done(n_item);
+        if (ntot > 0) ++n_act;
+      }
+      if (!ok) *sAbort = 1;
     }
   } else {
     // ------------------------------------------------------------------ softmax (half a row per thread)
     // Every softmax warp of a tile reaches the tile's barriers; a bounded wait that gave up only marks the tile bad,
     // and a barrier's OR decides for all of them.
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;\n");
     const int w = warp >> 3, hf = (warp >> 2) & 1, tr = (warp & 3) * 32 + lane;  // tile, key half, row of the tile
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    // S of my keys (their P goes over its first 32 columns), O of my channels
+    // S of my keys (their P goes over its first 32 columns)
     const uint32_t sb = trow + kColS + w * kNk + 64 * hf;
-    const uint32_t ob = trow + kColO + w * kD + 64 * hf;
+    const uint32_t ob = trow + kColO + w * kD + 64 * hf;  // O of my channels (rescaling)
     float* side = sSide + (2 * w + hf) * kTileRows + tr;
     float* other = sSide + (2 * w + (hf ^ 1)) * kTileRows + tr;
     const float inv_heads = 1.f / static_cast<float>(p.n_heads);
     bool ok = true;
     for (; ok; ++n_item) {
-      if (named_sync_or(1 + w, kTileThreads, !item_wait(n_item))) {
-        ok = false;
-        break;
-      }
+      if (MODE == kBounded)
+        ok = item_wait(n_item);
+      else  // a barrier's OR, so that the warps of a tile leave together
+        ok = !named_sync_or(1 + w, kTileThreads, !item_wait(n_item));
+      if (!ok) break;
       const ItemDesc& d = items[n_item % kItems];
       const int row = d.row0 + w * kTileRows + tr;
       if (d.row0 < 0) break;
@@ -945,68 +1013,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      // epilogue: O / l in bf16 (64 channels per thread), and the log-sum-exp
+      // the row's sum and what it stands on, once the output warps have read the last item's
       if constexpr (MODE == kBounded) {
         l_a = __fadd2_rn(l_a, l_b);
         l_run = l_a.x + l_a.y;
         m_used = ref;
-        shift = 0;
+      } else {
+        m_used -= slope2 * static_cast<float>(shift);
       }
-      *side = l_run;
-      const bool done = it == 0 || fail || __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status));
-      tc_fence_after();
-      if (named_sync_or(1 + w, kTileThreads, !done || fail)) {
-        ok = false;
-        break;
-      }
-      l_run += *other;
-      const bool has = in && l_run > 0.f;
-      const float inv = has ? 1.f / l_run : 0.f;
-      float odd = 0.f;  // NaN once an output is not finite
-#pragma unroll 1
-      for (int c = 0; c < 64; c += 16) {
-        uint32_t o[16], v[8];
-        if (it > 0) {
-          tmem_ld16(ob + c, o);
-          tmem_ld_wait();
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          o[e] = has ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
-          odd = fmaf(__uint_as_float(o[e]), 0.f, odd);
-        }
-        if (p.rope_dims > 0 && has) rope16(o, 64 * hf + c, p, t);  // the output's last rope_dims channels
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = pack_bf16(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-        if (in) store32(p.out + (int64_t)row * kD + 64 * hf + c, v);
-      }
-      // the next item's first P V overwrites O: this warp's reads of it are complete
-      tc_fence_before();
+      ok = !fail && __all_sync(kFull, n_item == 0 || mbar_wait(&lfree[w], (n_item - 1) & 1u, p.status));
+      if (MODE != kBounded) ok = !named_sync_or(1 + w, kTileThreads, !ok);
+      if (!ok) break;
+      sSum[(2 * w + hf) * kTileRows + tr] = l_run;
+      if (hf == 0) sBase[w * kTileRows + tr] = m_used;
       __syncwarp();
-      if (it > 0 && lane == 0) mbar_arrive(&oread[w]);
-      float lse = has ? (m_used + log2f(l_run) - slope2 * static_cast<float>(shift)) * kLn2 : -INFINITY;
-      const unsigned redo = __ballot_sync(kFull, in && (l_run != l_run || !(odd == 0.f)));
-      if (redo) {  // rows to take again, my channels of them, over what their threads stored
-        __syncwarp();
-        for (unsigned left = redo; left; left &= left - 1) {
-          const int b = __ffs(left) - 1;  // one row at a time, by the whole warp
-          const int rr = __shfl_sync(kFull, row, b);
-          float o4[4], m, l;
-          slow_row<CAP>(p, rr, r.pre.x, r.cap2.x, __shfl_sync(kFull, slope2, b), o4, m, l, lane);
-          const float iv = 1.f / l;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o4[e] *= iv;
-          inverse_rope4(o4, 4 * lane, kD, p.rope_dims, p.rope_base, __shfl_sync(kFull, t, b));
-          if (lane >> 4 == hf)
-            *reinterpret_cast<uint2*>(p.out + (int64_t)rr * kD + 4 * lane) =
-                make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
-          if (lane == b) lse = (m + log2f(l)) * kLn2;
-        }
-      }
-      if (in && hf == 0 && p.lse) p.lse[row] = lse;
+      if (lane == 0) mbar_arrive(&lready[w]);
       item_done(n_item);
       g += it;
-      if (it > 0) ++n_act;
     }
     if (!ok) *sAbort = 1;
   }
@@ -1032,12 +1055,13 @@ bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box
 
 }  // namespace
 
-// The plain form (no rule) keeps the kernels it has always run on, and so its results.
+// The plain form (no rule) keeps the kernels it has always run on, and so its results. Inverse RoPE stays with the
+// query-pair and split kernels: its fp64 sine and cosine do not fit the output warps' registers.
 bool attend_chunk_supported(const AttendParams& p, int n_sm) {
   const uint64_t pool_rows = static_cast<uint64_t>(p.n_pages) * p.page_size;
   const uint64_t ring_rows = static_cast<uint64_t>(p.n_seqs_layer) * p.n_win;
   const int64_t rows = (int64_t)p.n_q * p.n_heads;
-  return !p.is_csa && has_score_rule(p) && p.x_chunk && p.d_qk == kD && p.d_v == kD && p.n_heads >= 16 &&
+  return !p.is_csa && has_score_rule(p) && p.x_chunk && p.rope_dims == 0 && p.d_qk == kD && p.d_v == kD && p.n_heads >= 16 &&
          p.kv_dtype == CSKV_BF16 && rows >= (int64_t)kItemRows * n_sm / 2 && rows <= 0x7fffffff - (int64_t)kItemRows * (n_sm + 1) &&
          p.max_pos < (1 << 30) && p.n_win < (1 << 30) && p.chunk_len > 0 &&
          pool_rows <= kRowMask && ring_rows <= kRowMask && static_cast<uint64_t>(p.chunk_len) <= kRowMask;

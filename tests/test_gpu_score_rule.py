@@ -129,7 +129,7 @@ class Setup:
             ent = raw[:0]
         return torch.cat([raw, ent]), torch.cat([p.double(), j.double() * self.m + (self.m - 1) / 2])
 
-    def check(self, out, lse, cap, slopes, queries=None, scale=None):
+    def check(self, out, lse, cap, slopes, queries=None, rope=0):
         for i in range(len(self.positions)) if queries is None else queries:
             rows, pos = self.rows(i)
             q = self.q[i].double()
@@ -148,7 +148,17 @@ class Setup:
             D = q.shape[1] * 2.0 ** -24 * sm * (q.abs() @ rows.abs().t()).amax(1)
             D = D + 2.0 ** -20 * s.abs().amax(1) + 2.0 ** -22 * bias.abs().clamp(max=100).amax(1)
             wv = w @ v.abs()
-            tol = (2 * D[:, None] + 2.0 ** -8 + 2.0 ** -16) * wv + (2 * D[:, None] + 2.0 ** -8) * o.abs()
+            tol = (2 * D[:, None] + 2.0 ** -8 + 2.0 ** -16) * wv + 2 * D[:, None] * o.abs()
+            if rope:  # pairs of the last channels rotated by -t theta: so are their bounds, and cos, sin in fp32
+                c0 = self.d_v - rope
+                k = torch.arange(rope // 2, device="cuda", dtype=torch.float64)
+                ang = self.positions[i] * 10000.0 ** (-2 * k / rope)
+                c, n = torch.cos(ang), torch.sin(ang)
+                a, b = o[:, c0::2].clone(), o[:, c0 + 1::2].clone()
+                ta, tb = tol[:, c0::2] + 2.0 ** -20 * a.abs(), tol[:, c0 + 1::2] + 2.0 ** -20 * b.abs()
+                o[:, c0::2], o[:, c0 + 1::2] = a * c + b * n, b * c - a * n
+                tol[:, c0::2], tol[:, c0 + 1::2] = ta * c.abs() + tb * n.abs(), tb * c.abs() + ta * n.abs()
+            tol = tol + 2.0 ** -8 * o.abs()
             err = (out[i].double() - o).abs()
             assert bool((err <= tol).all()), "query %d (t = %d): off by %.3g of its bound" % (
                 i, self.positions[i], float((err / tol).max()))
@@ -277,18 +287,8 @@ def test_inverse_rope_and_no_lse(ck):
     for d_qk, d_v, H, n_q in ((128, 128, 32, 2), (576, 512, 64, 2), (128, 128, 64, 640)):
         pos = [3000 + i for i in range(n_q)]
         s = Setup(ck, "hca", d_qk, d_v, H, [0] * n_q, pos, seed=13, chunk={0: (0, 3000, n_q)})
-        plain, _ = s.run(30.0, s.slopes)
         out, _ = s.run(30.0, s.slopes, lse=False, rope_dims=32)
-        c0 = d_v - 32
-        assert torch.equal(out[..., :c0], plain[..., :c0])
-        i = torch.arange(16, device="cuda", dtype=torch.float64)
-        ang = s.q_pos.double()[:, None] * 10000.0 ** (-2 * i / 32)
-        a, b = plain[..., c0::2].double(), plain[..., c0 + 1::2].double()
-        c, n = torch.cos(ang)[:, None], torch.sin(ang)[:, None]
-        for got, want in ((out[..., c0::2].double(), a * c + b * n), (out[..., c0 + 1::2].double(), b * c - a * n)):
-            # both sides rounded: half a step of each input and of the result
-            tol = 2.0 ** -8 * (a.abs() + b.abs() + want.abs()) + 1e-6
-            assert bool(((got - want).abs() <= tol).all())
+        s.check(out, None, 30.0, s.slopes, sorted({0, n_q // 2, n_q - 1}), rope=32)
 
 
 def test_masked_keys_keep_out(ck):
