@@ -51,6 +51,7 @@
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
+#include "tc_issue.cuh"
 
 namespace cskv {
 namespace {
@@ -194,38 +195,6 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
       : "memory");
   return r != 0;
 }
-// The MMAs are issued by one elected lane, but by code that the whole warp runs together: the descriptors then sit in
-// uniform registers. Inside a branch on the lane every one of them is moved there first, which held an MMA up for
-// ~140 cycles (64 is what it takes to run).
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void umma_ss_if(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
-      : "memory");
-}
-__device__ __forceinline__ void umma_ts_if(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
-      : "memory");
-}
-__device__ __forceinline__ void commit_if(uint32_t issue, uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(issue)
-      : "memory");
-}
-
 // 32 bytes, a whole sector per thread
 __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),

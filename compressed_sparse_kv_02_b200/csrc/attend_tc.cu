@@ -51,6 +51,7 @@
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
+#include "tc_issue.cuh"
 
 namespace cskv {
 namespace {
@@ -192,16 +193,16 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
 
 // S of one key tile: 9 channel blocks x 4 K-steps (M = 64 heads, N = 64 keys); even blocks
 // accumulate at d (lanes +0), odd blocks at d + 16 lanes, the two chains issued alternately
-__device__ __forceinline__ void issue_s(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+__device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
 #pragma unroll
   for (int s = 0; s < 20; ++s) {
     const int ia = 2 * (s >> 2), ks = s & 3;
-    umma_ss(d, umma_desc_sw128(q + ia * kBlkBytes + ks * 32, 16, 1024),
-            umma_desc_sw128(k + ia * kBlkBytes + ks * 32, 16, 1024), idesc, s > 0 ? 1u : 0u);
+    umma_ss_if(issuer, d, umma_desc_sw128(q + ia * kBlkBytes + ks * 32, 16, 1024),
+               umma_desc_sw128(k + ia * kBlkBytes + ks * 32, 16, 1024), idesc, s > 0 ? 1u : 0u);
     if (s < 16) {
       const int ib = ia + 1;
-      umma_ss(d + kLane16, umma_desc_sw128(q + ib * kBlkBytes + ks * 32, 16, 1024),
-              umma_desc_sw128(k + ib * kBlkBytes + ks * 32, 16, 1024), idesc, s > 0 ? 1u : 0u);
+      umma_ss_if(issuer, d + kLane16, umma_desc_sw128(q + ib * kBlkBytes + ks * 32, 16, 1024),
+                 umma_desc_sw128(k + ib * kBlkBytes + ks * 32, 16, 1024), idesc, s > 0 ? 1u : 0u);
     }
   }
 }
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* sPref = reinterpret_cast<int*>(sm + Sm::PREF);
   __shared__ int s_wsum[32];
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int groups = p.n_heads / kH;
   const int kps = p.keys_per_split;
 
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sTmem;
+  const uint32_t tmem = __shfl_sync(kFull, *sTmem, 0);
   // the set-up above overlaps the tail of the kernel launched before this one; its
   // outputs (the selection, new cache rows) are read only from here on
   grid_dependency_wait();
@@ -563,27 +564,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 4) {
       // ------------------------------------------------------------ S issue (lane 0; the warp waits together)
-      const bool issuer = lane == 0;
-      const uint32_t idesc_s = umma_idesc_bf16(kH, kNk, false);
+      const uint32_t issuer = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kH, kNk, false);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
       bool ok = __all_sync(kFull, mbar_wait(qbar, n_item & 1u, p.status));
       tc_fence_after();
       for (int it = 0; it < ntiles && ok; ++it) {
         if (__shfl_sync(kFull, *sAbort, 0)) break;
         const uint32_t gt = g + it;
-        const int k = gt & 1;
+        const int k = __shfl_sync(kFull, gt & 1, 0);
         // the stage is shared memory written by TMA or fenced cp.async / stores: the mbarrier
         // orders it; S buffer k is free once the softmax has read S(gt - 2)
         if (!(ok = __all_sync(kFull, mbar_wait(&kfull[k], (gt >> 1) & 1u, p.status)))) break;
         if (gt >= 2 && !(ok = __all_sync(kFull, mbar_wait(&sfree[k], ((gt >> 1) - 1) & 1u, p.status)))) break;
         tc_fence_after();
-        if (issuer) {
-          issue_s(tmem + kColS + k * kNk, sQa, sKa + k * kStageBytes, idesc_s);
-          umma_commit(&sfull[k]);
-        }
+        if (k == 0)  // the stage as a constant in each branch, so that the descriptors are
+          issue_s(issuer, tmem + kColS, sQa, sKa, idesc_s);
+        else
+          issue_s(issuer, tmem + kColS + kNk, sQa, sKa + kStageBytes, idesc_s);
+        commit_if(issuer, &sfull[k]);
         __syncwarp();
       }
-      if (!ok && issuer) *sAbort = 1;
+      if (!ok && lane == 0) *sAbort = 1;
       __syncwarp();
     } else if (warp < 4) {
       // ------------------------------------------------------------ softmax
@@ -592,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sl2 = cap2 > 0.f ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
       const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
       const int hr = warp * 16 + (lane & 15), kh = lane >> 4;
-      const uint32_t idesc_pv = umma_idesc_bf16(kH, 256, true);
+      const uint32_t issuer = elect_one();
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(kH, 256, true);
       const uint32_t sKa = smem_u32(sK), sPa = smem_u32(sP);
       const float slope2 = RULE && p.slopes ? p.slopes[grp * kH + hr] * kLog2e : 0.f;
       uint8_t* prow = sP + hr * 128;
@@ -706,22 +709,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        if (tid == 0) {
+        if (warp == 0) {
           tc_fence_after();
-          const uint32_t vb = sKa + k * kStageBytes;  // channel blocks 0..7 of the tile: V
+          auto issue_pv = [&](uint32_t vb) {  // channel blocks 0..7 of the tile: V
 #pragma unroll
-          for (int ks = 0; ks < kNk / 16; ++ks) {
-            const uint64_t pa = umma_desc_sw128(sPa + ks * 32, 16, 1024);
-            const uint32_t acc = (it > 0 || ks > 0) ? 1u : 0u;
-            umma_ss(tmem + kColO, pa, umma_desc_sw128(vb + ks * 16 * 128, kBlkBytes, 1024), idesc_pv, acc);
-            umma_ss(tmem + kColO + kLane16, pa, umma_desc_sw128(vb + 4 * kBlkBytes + ks * 16 * 128, kBlkBytes, 1024),
-                    idesc_pv, acc);
-          }
-          umma_commit(&kempty[k]);
-          umma_commit(obar);
+            for (int ks = 0; ks < kNk / 16; ++ks) {
+              const uint64_t pa = umma_desc_sw128(sPa + ks * 32, 16, 1024);
+              const uint32_t acc = (it > 0 || ks > 0) ? 1u : 0u;
+              umma_ss_if(issuer, tmem + kColO, pa, umma_desc_sw128(vb + ks * 16 * 128, kBlkBytes, 1024), idesc_pv, acc);
+              umma_ss_if(issuer, tmem + kColO + kLane16, pa,
+                         umma_desc_sw128(vb + 4 * kBlkBytes + ks * 16 * 128, kBlkBytes, 1024), idesc_pv, acc);
+            }
+          };
+          if (__shfl_sync(kFull, k, 0) == 0)
+            issue_pv(sKa);
+          else
+            issue_pv(sKa + kStageBytes);
+          commit_if(issuer, &kempty[k]);
+          commit_if(issuer, obar);
+          __syncwarp();
         }
       }
-      if (tid == 0) umma_commit(dbar);  // one completion per item, also after an abort
+      if (warp == 0) commit_if(issuer, dbar);  // one completion per item, also after an abort
       // epilogue: normalised partial output of this split and head group, and its log-sum-exp
       ok = __all_sync(kFull, mbar_wait(dbar, n_item & 1u, p.status)) && ok;
       if (!ok) *sAbort = 1;

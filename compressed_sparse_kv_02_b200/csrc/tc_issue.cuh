@@ -1,0 +1,44 @@
+// tc_issue.cuh -- tcgen05.mma issued by one elected lane of a warp that runs the issuing code together.
+//
+// The descriptors then sit in uniform registers, where the instruction wants them. Inside a branch on the lane every
+// one of them is moved there first, which held an MMA up for 110-140 cycles whatever its shape (an M = N = 128 one
+// runs for 64). For the compiler to see that a value is the same in every lane it has to come from a kernel argument, a
+// constant, a vote or a shuffle from a constant lane.
+#pragma once
+
+#include <stdint.h>
+
+#include "cskv_device.cuh"
+
+namespace cskv {
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void umma_ss_if(uint32_t issue, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_if(uint32_t issue, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t issue, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
+}
+
+}  // namespace cskv
