@@ -17,7 +17,7 @@
 //     then cp.async of the 2 x 64 rows (16 threads per 256-byte row) into a
 //     128-byte-swizzled stage (four stages: the loaders run up to three tiles
 //     ahead, so the hand-offs of consecutive tiles overlap); Q of the pair by TMA;
-//   MMA (warp 4, lane 0 issues): S(t) = Q K^T (2 x 8 MMAs, M = 64, N = 64, K = 16)
+//   MMA (warp 4, one lane issues): S(t) = Q K^T (2 x 8 MMAs, M = 64, N = 64, K = 16)
 //     into S buffer t & 1; then O += P(t - 1) V (2 x 4 MMAs, N = d_v = 128, V read
 //     MN-major from the same stage: V is the first d_v channels of each key);
 //   softmax (warps 0-3): max pass over S(t) in tensor memory, lazy O rescale,
@@ -37,6 +37,7 @@
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
+#include "tc_issue.cuh"
 
 namespace cskv {
 namespace {
@@ -147,21 +148,22 @@ __device__ __forceinline__ void named_sync(int id, int n) {
 }
 
 // S of one query: 8 MMAs (K = 16 channels each) over the two 64-channel halves (N = 64 keys)
-__device__ __forceinline__ void issue_s(uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+__device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
     const uint32_t off = (ks & 3) * 32u;
-    umma_ss(d, umma_desc_sw128(q + (ks >> 2) * (kH * 128) + off, 16, 1024),
-            umma_desc_sw128(k + (ks >> 2) * kHalfBytes + off, 16, 1024), idesc, ks > 0 ? 1u : 0u);
+    umma_ss_if(issuer, d, umma_desc_sw128(q + (ks >> 2) * (kH * 128) + off, 16, 1024),
+               umma_desc_sw128(k + (ks >> 2) * kHalfBytes + off, 16, 1024), idesc, ks > 0 ? 1u : 0u);
   }
 }
 // O += P V of one query: 4 MMAs (K = 16 keys each; P is one 64-key swizzle atom); V MN-major
 // (its two 64-channel halves kHalfBytes apart, 8-key groups 1024 bytes apart)
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pm, uint32_t v, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void issue_pv(uint32_t issuer, uint32_t d, uint32_t pm, uint32_t v, uint32_t idesc,
+                                         bool acc) {
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks)
-    umma_ss(d, umma_desc_sw128(pm + ks * 32, 16, 1024),
-            umma_desc_sw128(v + ks * 16 * 128, kHalfBytes, 1024), idesc, (acc || ks > 0) ? 1u : 0u);
+    umma_ss_if(issuer, d, umma_desc_sw128(pm + ks * 32, 16, 1024),
+               umma_desc_sw128(v + ks * 16 * 128, kHalfBytes, 1024), idesc, (acc || ks > 0) ? 1u : 0u);
 }
 
 // Pipeline (tiles numbered gt across the CTA's items; stage gt % 4, S buffer gt & 1,
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
   float* sDist = reinterpret_cast<float*>(sm + Smem::DIST);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNS; ++i) {
       mbar_init(&kfull[i], 1);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sTmem;
+  const uint32_t tmem = __shfl_sync(kFull, *sTmem, 0);
   // the set-up above overlaps the tail of the kernel ahead of this one; its outputs
   // (the selection, new cache rows) are read only from here on
   grid_dependency_wait();
@@ -372,51 +374,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 4) {
       // ---------------------------------------------------------------- MMA issue
-      // The whole warp takes every wait (it never diverges around a barrier); lane 0 issues the
-      // MMAs and their commits.
-      const bool issuer = lane == 0;
-      const uint32_t idesc_s = umma_idesc_bf16(kH, kNk, false);
-      const uint32_t idesc_pv = umma_idesc_bf16(kH, kD, true);
+      // The whole warp takes every wait (it never diverges around a barrier); one elected lane issues
+      // the MMAs and their commits.
+      const uint32_t issuer = elect_one();
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kH, kNk, false);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(kH, kD, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sPa = smem_u32(sP);
+      const uint32_t slot1 = __shfl_sync(kFull, shared ? 0 : kSlotBytes, 0);  // the second query's key tile
       bool ok = __all_sync(kFull, mbar_wait(qfull, n_item & 1u, p.status));
       tc_fence_after();
       for (int it = 0; it <= ntiles && ok; ++it) {
         if (__shfl_sync(kFull, *sAbort, 0)) break;
         if (it < ntiles) {
-          const uint32_t gt = g + it;
+          const uint32_t gt = __shfl_sync(kFull, g + it, 0);
           const int st = gt % kNS;
           if (!(ok = __all_sync(kFull, mbar_wait(&kfull[st], (gt / kNS) & 1u, p.status)))) break;
           tc_fence_after();
-          if (issuer) {
-            const uint32_t d = tmem + kColS + (gt & 1u) * kNk;
-            const uint32_t kb = sKa + st * kStageBytes;
-            issue_s(d, sQa, kb, idesc_s);
-            issue_s(d + (16u << 16), sQa + kQBytes / 2, shared ? kb : kb + kSlotBytes, idesc_s);
-            umma_commit(&sfull[gt & 1u]);
-            if (it == ntiles - 1) umma_commit(qempty);
-          }
+          const uint32_t d = tmem + kColS + (gt & 1u) * kNk;
+          const uint32_t kb = sKa + st * kStageBytes;
+          issue_s(issuer, d, sQa, kb, idesc_s);
+          issue_s(issuer, d + (16u << 16), sQa + kQBytes / 2, kb + slot1, idesc_s);
+          commit_if(issuer, &sfull[gt & 1u]);
+          if (it == ntiles - 1) commit_if(issuer, qempty);
           __syncwarp();
         }
         if (it >= 1) {
-          const uint32_t gp = g + it - 1;
+          const uint32_t gp = __shfl_sync(kFull, g + it - 1, 0);
           const int pb = gp & 1u, sp = gp % kNS;
           if (!(ok = __all_sync(kFull, mbar_wait(&pfull[pb], (gp >> 1) & 1u, p.status)))) break;
           tc_fence_after();
-          if (issuer) {
-            const uint32_t vb = sKa + sp * kStageBytes, pm = sPa + pb * kPBytes;
-            issue_pv(tmem + kColO, pm, vb, idesc_pv, it > 1);
-            issue_pv(tmem + kColO + (16u << 16), pm + kPBytes / 2, shared ? vb : vb + kSlotBytes, idesc_pv, it > 1);
-            umma_commit(&kempty[sp]);
-            umma_commit(&obar[pb]);
-          }
+          const uint32_t vb = sKa + sp * kStageBytes, pm = sPa + pb * kPBytes;
+          issue_pv(issuer, tmem + kColO, pm, vb, idesc_pv, it > 1);
+          issue_pv(issuer, tmem + kColO + (16u << 16), pm + kPBytes / 2, vb + slot1, idesc_pv, it > 1);
+          commit_if(issuer, &kempty[sp]);
+          commit_if(issuer, &obar[pb]);
           __syncwarp();
         }
       }
-      if (issuer) {
-        if (ntiles == 0) umma_commit(qempty);
-        umma_commit(dbar);  // one completion per item, also after an abort
-        if (!ok) *sAbort = 1;
-      }
+      if (ntiles == 0) commit_if(issuer, qempty);
+      commit_if(issuer, dbar);  // one completion per item, also after an abort
+      if (lane == 0 && !ok) *sAbort = 1;
       __syncwarp();
     } else if (warp < 4) {
       // ---------------------------------------------------------------- softmax (one head row per thread)
@@ -613,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // after an abort, give tensor-core work and copies in flight a bounded chance to land (each
   // warp decides on lane 0's reading of the flag, so it stays converged)
   if (warp == 4 && __shfl_sync(kFull, *sAbort, 0)) {
-    if (lane == 0) umma_commit(dbar);
+    commit_if(elect_one(), dbar);
     __syncwarp();
     mbar_wait(dbar, n_item & 1u, nullptr);
   }
