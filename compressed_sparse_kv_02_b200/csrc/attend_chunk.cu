@@ -185,16 +185,6 @@ __device__ __forceinline__ uint32_t range_bits(int a, int lo, int hi) {
   return h > l ? (0xffffffffu >> (32 - (h - l))) << l : 0u;
 }
 
-// named barrier over n threads that also returns the OR of `v` over them (the same in every thread)
-__device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred q, p;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
 // 32 bytes, a whole sector per thread
 __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),

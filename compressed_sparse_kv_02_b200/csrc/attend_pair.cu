@@ -65,8 +65,8 @@ struct Smem {
   static constexpr int Q = 0;
   static constexpr int K = Q + kQBytes;
   static constexpr int P = K + kNS * kStageBytes;
-  static constexpr int ROWS = P + 2 * kPBytes;    // source-row codes of the tile being issued
-  static constexpr int BAR = ROWS + kRows * 4;
+  static constexpr int ROWS = P + 2 * kPBytes;    // [2] source-row codes of the tile being issued, and the last one's
+  static constexpr int BAR = ROWS + 2 * kRows * 4;
   static constexpr int TMEM = BAR + (2 * kNS + 9) * 8;
   static constexpr int FLAGS = TMEM + 4;
   static constexpr int MASK = FLAGS + 8;          // valid-key bits: [stage][query][2 words]
@@ -106,33 +106,48 @@ __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
   return r;
 }
 
-// Code of the source row of key u (< k.n) of query b: window keys first (ring-slot order when
-// every window row is in the ring, position order when a prefill chunk supplies some), then the
-// compressed entries. 0 if the row is invalid.
-// dist: the key's distance from position k.t in tokens (RULE).
-__device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int seq, const Keys& k, int u,
-                                             float& dist) {
-  dist = 0.f;
+// The source row of one key, found in three steps a tile apart, so that no step waits for the loads of the one before
+// it: which key (its entry, through the selection), which page, which row.
+// Window keys come first (ring-slot order when every window row is in the ring, position order when a prefill chunk
+// supplies some), then the compressed entries. A code of 0 is an invalid row.
+struct Lookup {
+  uint32_t code;  // of a window row
+  int entry;      // else the entry, -1: none
+  int32_t page;   // and its page
+  float dist;     // the key's distance from position k.t in tokens (RULE)
+};
+// key u (< k.n) of query b
+__device__ __forceinline__ void look_key(const AttendParams& p, int b, int seq, const Keys& k, int u, Lookup& l) {
+  l.code = 0;
+  l.entry = -1;
+  l.dist = 0.f;
   if (u < k.n_w) {
     if (!p.x_chunk) {
-      dist = static_cast<float>((k.t - u) % p.n_win);  // slot u holds the latest position up to t that is u mod n_win
-      return (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + u);
+      l.dist = static_cast<float>((k.t - u) % p.n_win);  // slot u holds the latest position up to t that is u mod n_win
+      l.code = (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + u);
+      return;
     }
     const int64_t pos = k.ws + u;
-    dist = static_cast<float>(k.t - pos);
+    l.dist = static_cast<float>(k.t - pos);
     const int64_t cr = chunk_row(p, seq, pos);
-    if (cr >= 0) return (3u << kRowBits) | static_cast<uint32_t>(cr);
-    return (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + pos % p.n_win);
+    l.code = cr >= 0 ? (3u << kRowBits) | static_cast<uint32_t>(cr)
+                     : (2u << kRowBits) | static_cast<uint32_t>(seq * p.n_win + pos % p.n_win);
+    return;
   }
-  const int jj = u - k.n_w;
-  const int64_t j = p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k + jj]) : jj;
-  if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return 0;
-  dist = entry_distance(k.t, j, p.m);
+  l.entry = p.is_csa ? p.sel_idx[(int64_t)b * p.k + (u - k.n_w)] : u - k.n_w;
+}
+__device__ __forceinline__ void look_page(const AttendParams& p, int seq, const Keys& k, Lookup& l) {
+  l.page = -1;
+  const int64_t j = l.entry;
+  if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return;
+  l.dist = entry_distance(k.t, j, p.m);
   const int64_t pi = j / p.page_size;
-  if (pi >= p.max_pages_per_seq) return 0;
-  const int32_t page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
-  if (page < 0 || page >= p.n_pages) return 0;
-  return (1u << kRowBits) | static_cast<uint32_t>((int64_t)page * p.page_size + j % p.page_size);
+  if (pi < p.max_pages_per_seq) l.page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
+}
+__device__ __forceinline__ uint32_t look_row(const AttendParams& p, const Lookup& l) {
+  if (l.code) return l.code;
+  if (l.page < 0 || l.page >= p.n_pages) return 0;
+  return (1u << kRowBits) | static_cast<uint32_t>((int64_t)l.page * p.page_size + l.entry % p.page_size);
 }
 
 __device__ __forceinline__ const uint16_t* code_row(const AttendParams& p, uint32_t c) {
@@ -143,9 +158,6 @@ __device__ __forceinline__ const uint16_t* code_row(const AttendParams& p, uint3
   return nullptr;
 }
 
-__device__ __forceinline__ void named_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory");
-}
 
 // S of one query: 8 MMAs (K = 16 channels each) over the two 64-channel halves (N = 64 keys)
 __device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
@@ -168,7 +180,7 @@ __device__ __forceinline__ void issue_pv(uint32_t issuer, uint32_t d, uint32_t p
 
 // Pipeline (tiles numbered gt across the CTA's items; stage gt % 4, S buffer gt & 1,
 // P buffer gt & 1):
-//   loaders : wait kempty[stage] (P V of tile gt - 4 done) -> cp.async -> kfull[stage]
+//   loaders : wait kempty[stage] (P V of tile gt - 4 done) -> cp.async -> kfull of the tile before, once landed
 //   MMA     : wait kfull -> S(gt) -> commit sfull[gt & 1] (and qempty after an item's last S);
 //             wait pfull[(gt - 1) & 1] -> P V(gt - 1) -> commit kempty, obar[(gt - 1) & 1]
 //   softmax : wait sfull, kfull (valid-key bits) -> row max -> wait obar (P V of tile gt - 2
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sP = sm + Smem::P;
   uint32_t* sRow = reinterpret_cast<uint32_t*>(sm + Smem::ROWS);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Smem::BAR);
-  uint64_t* kfull = bars;               // [kNS] loaders -> MMA and softmax
+  uint64_t* kfull = bars;               // [kNS] loaders (128) -> MMA and softmax
   uint64_t* kempty = bars + kNS;        // [kNS] MMA -> loaders (commit after the tile's P V)
   uint64_t* sfull = bars + 2 * kNS;     // [2] MMA -> softmax
   uint64_t* pfull = sfull + 2;          // [2] softmax -> MMA (128 arrivals)
@@ -194,14 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* dbar = qempty + 1;          //     the item's last P V is done
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Smem::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Smem::FLAGS);
-  volatile int* sLdOk = sAbort + 1;
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
   float* sDist = reinterpret_cast<float*>(sm + Smem::DIST);
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kNS; ++i) {
-      mbar_init(&kfull[i], 1);
+      mbar_init(&kfull[i], kLoaders);
       mbar_init(&kempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -286,48 +297,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       // this thread's part of every tile: the source row of key (lt & 63) of query lt >> 6, and
-      // chunk (lt & 15) of rows (lt >> 4) + 8 q. A tile is signalled as soon as its copy has
-      // landed; the next tile's source rows are looked up after that, while the loaders wait
-      // for its stage.
+      // chunk (lt & 15) of rows (lt >> 4) + 8 q. The steps of a lookup run ahead of the tile they are for (the key
+      // three tiles, its page two), and a tile is signalled, by every loader thread, when its copies have
+      // landed, while the next tile's fly.
       const int chunk = lt & 15, half = chunk >> 3, c8 = chunk & 7;
       const int my_slot = lt >> 6, my_key = lt & (kNk - 1);
-      auto code_of = [&](int it, float& di) -> uint32_t {
-        uint32_t c = 0;
-        di = 0.f;
-        if (shared) {  // threads 0 .. kNk - 1: key lt of the shared list
-          const int u = it * kNk + lt;
-          if (lt < kNk && u < ksh.n) {
-            c = key_code(p, b1, s1, ksh, u, di);
-            if (!c) report(p.status, CSKV_ERR_OUT_OF_RANGE);
-          }
-          return c;
-        }
-        const int u = it * kNk + my_key;
-        if (u < (my_slot ? n1 : n0)) {
-          c = my_slot ? key_code(p, b1, s1, k1, u, di) : key_code(p, b0, s0, k0, u, di);
-          if (!c) report(p.status, CSKV_ERR_OUT_OF_RANGE);
-        }
-        return c;
+      const bool second = shared || my_slot;  // a shared list is that of query b1's last position
+      const Keys kl = shared ? ksh : my_slot ? k1 : k0;
+      const int bl = second ? b1 : b0, sl = second ? s1 : s0;
+      const int nl = shared ? (lt < kNk ? ksh.n : 0) : (my_slot ? n1 : n0);
+      auto key_at = [&](int it, Lookup& l) {
+        l.code = 0;
+        l.entry = -1;
+        const int u = it * kNk + (shared ? lt : my_key);
+        if (it < ntiles && u < nl) look_key(p, bl, sl, kl, u, l);
       };
-      float nd = 0.f;
-      uint32_t nc = ntiles > 0 ? code_of(0, nd) : 0u;
+      Lookup l0, l1, l2;  // of the tiles it, it + 1 (pages found) and it + 2 (keys found)
+      key_at(0, l0);
+      key_at(1, l1);
+      key_at(2, l2);
+      look_page(p, sl, kl, l0);
+      look_page(p, sl, kl, l1);
       for (int it = 0; it < ntiles; ++it) {
         const uint32_t gt = g + it;
         const int st = gt % kNS;
-        const uint32_t c = nc;
-        const float di = nd;
-        if (lw == 0) {
-          bool okw = __shfl_sync(kFull, *sAbort, 0) == 0;
-          if (okw && gt >= (uint32_t)kNS)
-            okw = __all_sync(kFull, mbar_wait(&kempty[st], ((gt / kNS) - 1) & 1u, p.status));
-          if (ll == 0) *sLdOk = okw;
-        }
-        named_sync(3, kLoaders);  // sLdOk is set (and the last tile's issue has read sRow)
-        if (!*sLdOk) {
-          *sAbort = 1;
-          break;
-        }
-        sRow[lt] = c;
+        const uint32_t c = look_row(p, l0);
+        const float di = l0.dist;
+        if (it * kNk + (shared ? lt : my_key) < nl && !c) report(p.status, CSKV_ERR_OUT_OF_RANGE);
+        const bool free =
+            __all_sync(kFull, gt < (uint32_t)kNS || mbar_wait(&kempty[st], ((gt / kNS) - 1) & 1u, p.status));
+        uint32_t* row_of = sRow + (gt & 1u) * kRows;
+        row_of[lt] = c;
         if (RULE) {
           if (!shared) {
             sDist[st * kRows + lt] = di;
@@ -353,24 +353,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned mw = __ballot_sync(kFull, c != 0);
           if ((lt & 31) == 0) sMask[st * 4 + (lt >> 5)] = mw;
         }
-        named_sync(3, kLoaders);
+        // the tile's rows are visible to every loader, or some wait gave up (the same answer for all)
+        if (named_sync_or(3, kLoaders, !free || *sAbort)) {
+          *sAbort = 1;
+          break;
+        }
         uint8_t* dst = sK + st * kStageBytes + half * kHalfBytes;
         const int n_q8 = shared ? kNk / 8 : kRows / 8;  // 8-row steps: one list or two
 #pragma unroll 4
         for (int q = 0; q < n_q8; ++q) {
           const int row = (lt >> 4) + 8 * q;  // query row / kNk, key row % kNk
           const int key = row & (kNk - 1);
-          const uint16_t* src = code_row(p, sRow[row]);
+          const uint16_t* src = code_row(p, row_of[row]);
           cp_async16(dst + (row / kNk) * kSlotBytes + key * 128 + ((c8 ^ (key & 7)) << 4),
                      src ? static_cast<const void*>(src + half * 64 + c8 * 8) : static_cast<const void*>(p.q),
                      src ? 16 : 0);
         }
         cp_async_commit();
-        cp_async_wait<0>();
+        l0 = l1;
+        l1 = l2;
+        look_page(p, sl, kl, l1);
+        key_at(it + 3, l2);
+        if (it > 0) {  // the tile before this one has landed
+          cp_async_wait<1>();
+          fence_proxy_async_smem();
+          mbar_arrive(&kfull[(gt - 1) % kNS]);
+        }
+      }
+      cp_async_wait<0>();
+      if (ntiles > 0 && !*sAbort) {
         fence_proxy_async_smem();
-        named_sync(3, kLoaders);
-        if (lt == 0) mbar_arrive(&kfull[st]);
-        if (it + 1 < ntiles) nc = code_of(it + 1, nd);
+        mbar_arrive(&kfull[(g + ntiles - 1) % kNS]);
       }
     } else if (warp == 4) {
       // ---------------------------------------------------------------- MMA issue

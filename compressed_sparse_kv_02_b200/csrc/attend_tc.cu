@@ -180,17 +180,6 @@ __device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 c) {
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory");
 }
-// named barrier over n threads that also returns the OR of `v` over them (the same in every thread)
-__device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred q, p;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, %3, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"(v ? 1u : 0u), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-
 // S of one key tile: 9 channel blocks x 4 K-steps (M = 64 heads, N = 64 keys); even blocks
 // accumulate at d (lanes +0), odd blocks at d + 16 lanes, the two chains issued alternately
 __device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
