@@ -178,6 +178,7 @@ struct Smem {
   static constexpr size_t bytes() { return 1024 + END; }
 };
 static_assert(Smem::bytes() <= 232448, "shared memory budget");
+static_assert(Smem::POS % 16 == 0 && Smem::ROWS % 16 == 0 && Smem::ITEM % 16 == 0 && Smem::BAR % 8 == 0, "alignment");
 
 // bits of lo <= u < hi for the 32 keys u = a .. a + 31
 __device__ __forceinline__ uint32_t range_bits(int a, int lo, int hi) {
@@ -192,122 +193,12 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8]) {
                : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
-  return r;
-}
-// a max of three, and of the magnitudes of three
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-  float r;
-  asm("max.abs.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// cap tanh(s pre) as a polynomial in s where |s pre| <= 1, to a relative error of 6e-7: tanh(u) / u in u^2 on [0, 1]
-// (fitted like tanh_rational), its coefficients times cap2 pre^(2i + 1). Logits seldom reach the cap, so most tiles
-// take this form: 7 fp32 operations a logit instead of 12, and no reciprocal.
-constexpr float kTanhP[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281434774398804f,
-                             -0.051605693995952606f, 0.016743136569857597f, -0.0030670680571347475f};
-// The rule's numbers, as a kernel argument: packed arithmetic then reads its constants, each a pair of the same number,
-// where they are instead of building the pairs in registers.
-struct Rule {
-  float2 pre, cap2;  // capped: sm_scale / cap and cap log2(e); else sm_scale log2(e) and 0
-  float2 c[6];
-  float lim;         // |s| up to here takes the polynomial (negative: never)
-};
-Rule make_rule(const AttendParams& p) {
-  const bool cap = p.score_cap > 0.f;
-  Rule r;
-  const float pre = cap ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e, cap2 = cap ? p.score_cap * kLog2e : 0.f;
-  r.pre = make_float2(pre, pre);
-  r.cap2 = make_float2(cap2, cap2);
-  r.lim = pre < 2048.f ? 1.f / pre : -1.f;  // above that pre^10 would leave fp32's range
-  float f = cap2 * pre;
-  for (int i = 0; i < 6; ++i) {
-    r.c[i] = make_float2(f * kTanhP[i], f * kTanhP[i]);
-    f *= pre * pre;
-  }
-  return r;
-}
-
 // The three forms of the kernel. kBounded: a cap of at most kMaxStatic (in log2 units) bounds every logit of a row to
 // [ref - cap2, ref + cap2] around a reference known beforehand, and the row's own token, or with a negative slope its
 // farthest key, reaches into that range, so 2^(s - ref) neither overflows fp32 nor vanishes, and the softmax needs no
 // running maximum: no pass for it, no agreement between the halves of a row, no rescaling (181 us -> STATIC us).
 enum Mode { kPlainMax, kCappedMax, kBounded };
 constexpr float kMaxStatic = 80.f;
-
-// The rule on N logits, two packed pairs in step: with the cap, without, or capped below lim. bias = slope2 * position
-// - ref, ref the row's running maximum so far (its subtraction costs nothing here).
-enum { kLinear, kRational, kPoly };
-template <int FORM, int N>
-__device__ __forceinline__ void rule_n(uint32_t (&s)[N], const float4* pos, const Rule& r, float2 slope,
-                                       float2 negref) {
-#pragma unroll
-  for (int b = 0; b < N; b += 4) {
-    const float4 pa = pos[b / 4];
-    float2 u[2] = {make_float2(__uint_as_float(s[b]), __uint_as_float(s[b + 1])),
-                   make_float2(__uint_as_float(s[b + 2]), __uint_as_float(s[b + 3]))};
-    const float2 bias[2] = {__ffma2_rn(slope, make_float2(pa.x, pa.y), negref), __ffma2_rn(slope, make_float2(pa.z, pa.w), negref)};
-    if constexpr (FORM == kLinear) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) u[j] = __ffma2_rn(u[j], r.pre, bias[j]);
-    } else if constexpr (FORM == kPoly) {
-      float2 x[2], n[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) x[j] = __fmul2_rn(u[j], u[j]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(r.c[5], x[j], r.c[4]);
-#pragma unroll
-      for (int i = 3; i >= 0; --i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(n[j], x[j], r.c[i]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) u[j] = __ffma2_rn(u[j], n[j], bias[j]);
-    } else {
-      float2 x[2], n[2], d[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        u[j] = __fmul2_rn(u[j], r.pre);
-        u[j] = make_float2(tanh_clamp(u[j].x), tanh_clamp(u[j].y));
-        x[j] = __fmul2_rn(u[j], u[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) d[j] = __ffma2_rn(make_float2(tanh_d(4), tanh_d(4)), x[j], make_float2(tanh_d(3), tanh_d(3)));
-#pragma unroll
-      for (int i = 2; i >= 0; --i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) d[j] = __ffma2_rn(d[j], x[j], make_float2(tanh_d(i), tanh_d(i)));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(make_float2(tanh_n(3), tanh_n(3)), x[j], make_float2(tanh_n(2), tanh_n(2)));
-#pragma unroll
-      for (int i = 1; i >= 0; --i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(n[j], x[j], make_float2(tanh_n(i), tanh_n(i)));
-#pragma unroll
-      for (int j = 0; j < 2; ++j) n[j] = __fmul2_rn(n[j], u[j]);
-      // two quotients share one reciprocal: 1 / d_a = d_b / (d_a d_b), each d at most 2^7.3
-      const float2 dd = __fmul2_rn(d[0], d[1]);
-      float2 rc;
-      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(rc.x) : "f"(dd.x));
-      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(rc.y) : "f"(dd.y));
-      rc = __fmul2_rn(rc, r.cap2);
-      u[0] = __ffma2_rn(__fmul2_rn(n[0], d[1]), rc, bias[0]);
-      u[1] = __ffma2_rn(__fmul2_rn(n[1], d[0]), rc, bias[1]);
-    }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s[b + 2 * j] = __float_as_uint(u[j].x);
-      s[b + 2 * j + 1] = __float_as_uint(u[j].y);
-    }
-  }
-}
 
 // One row from its own keys only, by one warp (lane = 4 channels): scores in fp32, an online softmax, fp32 P.
 template <bool CAP>
@@ -841,19 +732,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             tmem_ld32(sb + 32, sc);
             const float nr = -slope2 * static_cast<float>(shift) - ref;
-            const float2 negref = make_float2(nr, nr), sl = make_float2(slope2, slope2);
             const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf);
             auto part = [&](int c, uint32_t (&s)[32]) {
-              float big = 0.f, big1 = 0.f;
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                big = max3_abs(big, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-                big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-              }
-              if (__all_sync(kFull, fmaxf(big, big1) <= r.lim))
-                rule_n<kPoly>(s, pos4 + 8 * c, r, sl, negref);
-              else
-                rule_n<kRational>(s, pos4 + 8 * c, r, sl, negref);
+              apply_rule<true>(s, pos4 + 8 * c, r, slope2, nr);
               const int a = k * kNk + 64 * hf + 32 * c;
               const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, n_w, end));
               if (__any_sync(kFull, vm != kFull)) {
@@ -884,25 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
           tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
           tmem_ld_wait();
-          {
-            const float nr = m_used == -INFINITY ? 0.f : -m_used;
-            const float2 negref = make_float2(nr, nr), sl = make_float2(slope2, slope2);
-            const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf);
-            if constexpr (CAP) {
-              float big = 0.f, big1 = 0.f;
-#pragma unroll
-              for (int j = 0; j < 64; j += 4) {
-                big = max3_abs(big, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-                big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-              }
-              if (__all_sync(kFull, fmaxf(big, big1) <= r.lim))
-                rule_n<kPoly>(s, pos4, r, sl, negref);
-              else
-                rule_n<kRational>(s, pos4, r, sl, negref);
-            } else {
-              rule_n<kLinear>(s, pos4, r, sl, negref);
-            }
-          }
+          apply_rule<CAP>(s, reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf), r, slope2,
+                          m_used == -INFINITY ? 0.f : -m_used);
           float mt = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -1044,7 +908,7 @@ cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = (rows + kItemRows - 1) / kItemRows;
   return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q,
-                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, p, make_rule(p));
+                    tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, p, make_rule(p.sm_scale, p.score_cap));
 }
 
 }  // namespace cskv

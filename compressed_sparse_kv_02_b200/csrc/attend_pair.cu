@@ -66,15 +66,16 @@ struct Smem {
   static constexpr int K = Q + kQBytes;
   static constexpr int P = K + kNS * kStageBytes;
   static constexpr int ROWS = P + 2 * kPBytes;    // [2] source-row codes of the tile being issued, and the last one's
-  static constexpr int BAR = ROWS + 2 * kRows * 4;
+  static constexpr int DIST = ROWS + 2 * kRows * 4;  // RULE: minus the distances [stage][query][64 keys]
+  static constexpr int BAR = DIST + kNS * 2 * kNk * 4;
   static constexpr int TMEM = BAR + (2 * kNS + 9) * 8;
   static constexpr int FLAGS = TMEM + 4;
   static constexpr int MASK = FLAGS + 8;          // valid-key bits: [stage][query][2 words]
-  static constexpr int DIST = MASK + kNS * 2 * 2 * 4;  // RULE: distances [stage][query][64 keys]
-  static constexpr int END = DIST + kNS * 2 * kNk * 4;
+  static constexpr int END = MASK + kNS * 2 * 2 * 4;
   static constexpr size_t bytes() { return 1024 + END; }
 };
 static_assert(Smem::bytes() <= 232448, "shared memory budget");
+static_assert(Smem::DIST % 16 == 0 && Smem::BAR % 8 == 0 && Smem::MASK % 4 == 0, "alignment");
 
 // source-row code: kind in bits [31:30] (0 none, 1 pool entry, 2 ring row, 3 chunk row), row below
 constexpr uint32_t kRowBits = 30;
@@ -188,7 +189,7 @@ __device__ __forceinline__ void issue_pv(uint32_t issuer, uint32_t d, uint32_t p
 //             -> rescale O if needed (after P V of gt - 1) -> P(gt) -> arrive pfull
 template <bool RULE>
 __global__ void __launch_bounds__(kThreads, 1)
-    attend_pair_kernel(const __grid_constant__ CUtensorMap tm_q, AttendParams p) {
+    attend_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const AttendParams p, const __grid_constant__ Rule rule) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Smem::Q;
@@ -330,10 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         row_of[lt] = c;
         if (RULE) {
           if (!shared) {
-            sDist[st * kRows + lt] = di;
+            sDist[st * kRows + lt] = -di;
           } else if (lt < kNk) {  // one list for t and t + 1
-            sDist[st * kRows + lt] = di - 1.f;
-            sDist[st * kRows + kNk + lt] = di;
+            sDist[st * kRows + lt] = 1.f - di;
+            sDist[st * kRows + kNk + lt] = -di;
           }
         }
         if (shared) {  // loader warps 0 and 1 hold keys 32 w .. + 31 of the shared list
@@ -432,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- softmax (one head row per thread)
       const int slot = lane >> 4, h = warp * 16 + (lane & 15);
       const int b_mine = slot ? b1 : b0;
-      const float cap2 = RULE ? p.score_cap * kLog2e : 0.f;
-      const float sl2 = cap2 > 0.f ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
+      const float sl2 = p.sm_scale * kLog2e;
       const float slope2 = RULE && p.slopes ? p.slopes[h] * kLog2e : 0.f;
       const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
       uint8_t* prow = sP + slot * (kPBytes / 2) + h * 128;
@@ -460,21 +460,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's 64 logits of this row (two loads, one wait); the row max in four chains
         const uint64_t vm = static_cast<uint64_t>(valid[0]) | (static_cast<uint64_t>(valid[1]) << 32);
         float mt;
-        uint32_t ruled[RULE ? kNk : 1];  // RULE: the logits after the rule, in log2 units
+        uint32_t ruled[RULE ? kNk : 4];  // RULE: the logits after the rule, in log2 units
         if constexpr (RULE) {
           tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(ruled));
           tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(ruled + 32));
           tmem_ld_wait();
-          const float* dst = sDist + (gt % kNS) * kRows + slot * kNk;
-          if (cap2 > 0.f) {
-#pragma unroll
-            for (int j = 0; j < kNk; ++j)
-              ruled[j] = __float_as_uint(ruled_score<true>(__uint_as_float(ruled[j]), sl2, cap2, slope2, dst[j]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < kNk; ++j)
-              ruled[j] = __float_as_uint(ruled_score<false>(__uint_as_float(ruled[j]), sl2, 0.f, slope2, dst[j]));
-          }
+          const float4* pos = reinterpret_cast<const float4*>(sDist + (gt % kNS) * kRows + slot * kNk);
+          if (rule.cap2.x > 0.f)
+            apply_rule<true>(ruled, pos, rule, slope2, 0.f);
+          else
+            apply_rule<false>(ruled, pos, rule, slope2, 0.f);
           float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
           for (int j = 0; j < kNk; j += 2) {
@@ -667,7 +662,8 @@ cudaError_t launch_attend_pair(AttendParams& p, int n_sm, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int items = (p.n_q + 1) / 2;
   const int grid = items < n_sm ? items : n_sm;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, st, tm_q, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, st, tm_q, p,
+                    make_rule(p.sm_scale, p.score_cap));
 }
 
 }  // namespace cskv

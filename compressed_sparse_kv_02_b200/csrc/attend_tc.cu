@@ -87,7 +87,7 @@ struct Smem {
   static constexpr int P = K + kNS * kStageBytes;      // P of the tile (64 rows x 128 B)
   static constexpr int CODE = P + kPBytes;             // [kCodes][kNk] source-row codes of a stage's keys
   static constexpr int SCALE = CODE + kCodes * kNk * 4;  // [kNS][kNk] FP8 scale of each key (1 for bf16 rows)
-  static constexpr int DIST = SCALE + (FP8 ? kNS * kNk * 4 : 0);  // RULE: [kNS][kNk] distance of each key
+  static constexpr int DIST = SCALE + (FP8 ? kNS * kNk * 4 : 0);  // RULE: [kNS][kNk] minus the distance of each key
   static constexpr int MASK = DIST + (RULE || !FP8 ? kNS * kNk * 4 : 0);  // [kNS][2] valid-key bits
   static constexpr int BAR = MASK + 32;                // mbarriers
   static constexpr int TMEM = BAR + 16 * 8;            // allocated tensor-memory address
@@ -95,6 +95,8 @@ struct Smem {
   static constexpr int PREF = FLAGS + 16;              // [n_q + 1] items per query, exclusive prefix
   static size_t bytes(int n_q) { return 1024 + PREF + sizeof(int) * (size_t)(n_q + 1); }
 };
+
+static_assert(Smem<false, true>::DIST % 16 == 0 && Smem<true, true>::DIST % 16 == 0, "alignment");
 
 // source-row code: kind in bits [31:30] (0 none, 1 pool entry, 2 ring row, 3 chunk row), row below
 constexpr uint32_t kRowBits = 30;
@@ -209,7 +211,7 @@ template <bool FP8, bool RULE>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ring,
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvg,
-                     AttendParams p) {
+                     const AttendParams p, const __grid_constant__ Rule rule) {
   using Sm = Smem<FP8, RULE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lt < kNk) {
           sCode[lt] = code;
           if (FP8) sScale[st * kNk + lt] = code ? scale : 0.f;  // finite for every key of the tile
-          if (RULE) sDist[st * kNk + lt] = dist;
+          if (RULE) sDist[st * kNk + lt] = -dist;
         }
         if (lw < 2) {
           const unsigned bits = __ballot_sync(kFull, code != 0u);
@@ -579,8 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < 4) {
       // ------------------------------------------------------------ softmax
       // thread (warp, lane): head row hr = 16 warp + (lane & 15), keys 32 kh .. + 31 of each tile
-      const float cap2 = RULE ? p.score_cap * kLog2e : 0.f;
-      const float sl2 = cap2 > 0.f ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
+      const float sl2 = p.sm_scale * kLog2e;
       const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
       const int hr = warp * 16 + (lane & 15), kh = lane >> 4;
       const uint32_t issuer = elect_one();
@@ -622,17 +623,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (good) {
           const uint32_t vm = sMask[k * 2 + kh];
           const float* scl = sScale + k * kNk + 32 * kh;
-          const float* dst = sDist + k * kNk + 32 * kh;
           if (fp8) {  // an FP8 entry's logit and value carry its scale
 #pragma unroll
             for (int j = 0; j < 32; ++j) s[j] *= scl[j];
           }
-          if (RULE && cap2 > 0.f) {
+          if constexpr (RULE) {
+            const float4* pos = reinterpret_cast<const float4*>(sDist + k * kNk + 32 * kh);
+            uint32_t u[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = ruled_score<true>(s[j], sl2, cap2, slope2, dst[j]);
-          } else if (RULE) {
+            for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(s[j]);
+            if (rule.cap2.x > 0.f)
+              apply_rule<true>(u, pos, rule, slope2, 0.f);
+            else
+              apply_rule<false>(u, pos, rule, slope2, 0.f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] = ruled_score<false>(s[j], sl2, 0.f, slope2, dst[j]);
+            for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(u[j]);
           }
           const float post = RULE ? 1.f : sl2;  // the rule has scaled its logits
           float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
@@ -833,7 +838,7 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st) {
   const int grid = static_cast<int>(items < n_sm ? items : n_sm);
   p.part_t = 1;
   e = launch_pdl(kern, dim3(static_cast<unsigned>(grid < 1 ? 1 : grid)), dim3(kThreads), smem, st, tm_q, tm_ring,
-                 tm_kv, tm_kvg, p);
+                 tm_kv, tm_kvg, p, make_rule(p.sm_scale, p.score_cap));
   if (e != cudaSuccess) return e;
   return launch_attend_merge(p, st);
 }

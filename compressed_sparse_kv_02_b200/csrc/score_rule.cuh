@@ -42,4 +42,137 @@ __device__ __forceinline__ float entry_distance(int64_t t, int64_t j, int m) {
   return 0.5f * static_cast<float>(2 * (t - j * m) - (m - 1));
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+// a max of three, and of the magnitudes of three
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// cap tanh(s pre) as a polynomial in s where |s pre| <= 1, to a relative error of 6e-7: tanh(u) / u in u^2 on [0, 1]
+// (fitted like tanh_rational), its coefficients times cap2 pre^(2i + 1). Logits seldom reach the cap, so most tiles
+// take this form: 7 fp32 operations a logit instead of 12, and no reciprocal.
+constexpr float kTanhP[6] = {0.9999994039535522f, -0.3332904279232025f, 0.13281434774398804f,
+                             -0.051605693995952606f, 0.016743136569857597f, -0.0030670680571347475f};
+// The rule's numbers, as a kernel argument: packed arithmetic then reads its constants, each a pair of the same number,
+// where they are instead of building the pairs in registers.
+struct Rule {
+  float2 pre, cap2;  // capped: sm_scale / cap and cap log2(e); else sm_scale log2(e) and 0
+  float2 c[6];
+  float lim;         // |s| up to here takes the polynomial (negative: never)
+};
+inline Rule make_rule(float sm_scale, float score_cap) {
+  const float log2e = 1.4426950408889634f;
+  const bool cap = score_cap > 0.f;
+  Rule r;
+  const float pre = cap ? sm_scale / score_cap : sm_scale * log2e, cap2 = cap ? score_cap * log2e : 0.f;
+  r.pre = make_float2(pre, pre);
+  r.cap2 = make_float2(cap2, cap2);
+  r.lim = pre < 2048.f ? 1.f / pre : -1.f;  // above that pre^10 would leave fp32's range
+  float f = cap2 * pre;
+  for (int i = 0; i < 6; ++i) {
+    r.c[i] = make_float2(f * kTanhP[i], f * kTanhP[i]);
+    f *= pre * pre;
+  }
+  return r;
+}
+
+// The rule on N logits, two packed pairs in step: with the cap, without, or capped below lim. bias = slope2 * position
+// - ref, ref the row's running maximum so far (its subtraction costs nothing here).
+enum { kLinear, kRational, kPoly };
+template <int FORM, int N>
+__device__ __forceinline__ void rule_n(uint32_t (&s)[N], const float4* pos, const Rule& r, float2 slope,
+                                       float2 negref) {
+#pragma unroll
+  for (int b = 0; b < N; b += 4) {
+    const float4 pa = pos[b / 4];
+    float2 u[2] = {make_float2(__uint_as_float(s[b]), __uint_as_float(s[b + 1])),
+                   make_float2(__uint_as_float(s[b + 2]), __uint_as_float(s[b + 3]))};
+    const float2 bias[2] = {__ffma2_rn(slope, make_float2(pa.x, pa.y), negref), __ffma2_rn(slope, make_float2(pa.z, pa.w), negref)};
+    if constexpr (FORM == kLinear) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) u[j] = __ffma2_rn(u[j], r.pre, bias[j]);
+    } else if constexpr (FORM == kPoly) {
+      float2 x[2], n[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) x[j] = __fmul2_rn(u[j], u[j]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(r.c[5], x[j], r.c[4]);
+#pragma unroll
+      for (int i = 3; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(n[j], x[j], r.c[i]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) u[j] = __ffma2_rn(u[j], n[j], bias[j]);
+    } else {
+      float2 x[2], n[2], d[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        u[j] = __fmul2_rn(u[j], r.pre);
+        u[j] = make_float2(tanh_clamp(u[j].x), tanh_clamp(u[j].y));
+        x[j] = __fmul2_rn(u[j], u[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) d[j] = __ffma2_rn(make_float2(tanh_d(4), tanh_d(4)), x[j], make_float2(tanh_d(3), tanh_d(3)));
+#pragma unroll
+      for (int i = 2; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) d[j] = __ffma2_rn(d[j], x[j], make_float2(tanh_d(i), tanh_d(i)));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(make_float2(tanh_n(3), tanh_n(3)), x[j], make_float2(tanh_n(2), tanh_n(2)));
+#pragma unroll
+      for (int i = 1; i >= 0; --i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) n[j] = __ffma2_rn(n[j], x[j], make_float2(tanh_n(i), tanh_n(i)));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) n[j] = __fmul2_rn(n[j], u[j]);
+      // two quotients share one reciprocal: 1 / d_a = d_b / (d_a d_b), each d at most 2^7.3
+      const float2 dd = __fmul2_rn(d[0], d[1]);
+      float2 rc;
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(rc.x) : "f"(dd.x));
+      asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(rc.y) : "f"(dd.y));
+      rc = __fmul2_rn(rc, r.cap2);
+      u[0] = __ffma2_rn(__fmul2_rn(n[0], d[1]), rc, bias[0]);
+      u[1] = __ffma2_rn(__fmul2_rn(n[1], d[0]), rc, bias[1]);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      s[b + 2 * j] = __float_as_uint(u[j].x);
+      s[b + 2 * j + 1] = __float_as_uint(u[j].y);
+    }
+  }
+}
+
+// The rule on N logits of a row, in place: pos holds each key's position relative to some reference of the row's, and
+// negref what is added to every logit.
+template <bool CAP, int N>
+__device__ __forceinline__ void apply_rule(uint32_t (&s)[N], const float4* pos, const Rule& r, float slope2,
+                                           float negref) {
+  const float2 sl = make_float2(slope2, slope2), nr = make_float2(negref, negref);
+  if constexpr (CAP) {
+    float big = 0.f, big1 = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      big = max3_abs(big, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+      big1 = max3_abs(big1, __uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+    }
+    if (__all_sync(0xffffffffu, fmaxf(big, big1) <= r.lim))
+      rule_n<kPoly>(s, pos, r, sl, nr);
+    else
+      rule_n<kRational>(s, pos, r, sl, nr);
+  } else {
+    rule_n<kLinear>(s, pos, r, sl, nr);
+  }
+}
+
 }  // namespace cskv
