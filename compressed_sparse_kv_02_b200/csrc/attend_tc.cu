@@ -62,11 +62,15 @@ constexpr int kBlkBytes = kNk * 128;            // 8192: one channel block of a 
 constexpr int kStageBytes = kNb * kBlkBytes;    // 73728: a key tile (also the Q block set)
 constexpr int kNS = 2;                          // key-tile stages
 constexpr int kPBytes = kH * kNk * 2;           // 8192: P of the tile (bf16)
-constexpr int kThreads = 256;                   // warps 0-3 softmax, warp 4 S, warps 5-7 loads
-constexpr int kLoadThread0 = 160;
-constexpr int kLoaders = kThreads - kLoadThread0;  // 96
+constexpr int kLoadThread0 = 160;               // warps 0-3 softmax, warp 4 S, then the loaders
+// Loader warps: three for bf16 entries; seven for FP8, whose widening to bf16 is what such a tile's time goes to (three
+// took MIXED3 us for the mixed workload's selection, seven MIXED7), with registers moved to the softmax warps.
+template <bool FP8>
+struct Block {
+  static constexpr int kThreads = FP8 ? 384 : 256;
+  static constexpr int kLoaders = kThreads - kLoadThread0;  // 96 or 224
+};
 constexpr int kChunks = kNk * kNb * 8;          // 16-byte chunks of a bf16 tile (4608)
-constexpr int kPer = (kChunks + kLoaders - 1) / kLoaders;  // 48
 constexpr uint32_t kTmemCols = 512;
 // O[:, 0:256] lanes +0 and O[:, 256:512] lanes +16 of columns 0-255; S buffer k at columns
 // 256 + 64 k (even channel blocks at lanes +0, odd ones at lanes +16)
@@ -128,33 +132,48 @@ __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
   return r;
 }
 
-// Code of the source row of key u: window keys first, in ring-slot order (slot
-// u) when every window row is in the ring, in position order when a prefill
-// chunk supplies some of them; then the compressed entries. 0 if invalid.
-// dist: the key's distance from the query in tokens (RULE).
-__device__ __forceinline__ uint32_t key_code(const AttendParams& p, int b, int seq, const Keys& k, int64_t u,
-                                             float& dist) {
-  dist = 0.f;
+// The source row of one key, found in three steps a tile apart, so that no step waits for the loads of the one before
+// it: which key (its entry, through the selection), which page, which row (and scale).
+// Window keys come first, in ring-slot order (slot u) when every window row is in the ring, in position order when a
+// prefill chunk supplies some of them; then the compressed entries. A code of 0 is an invalid row.
+struct Lookup {
+  uint32_t code;  // of a window row
+  int32_t page;   // of an entry's
+  int64_t entry;  // the entry, -1: none
+  float dist;     // the key's distance from the query in tokens (RULE)
+};
+__device__ __forceinline__ void look_key(const AttendParams& p, int b, int seq, const Keys& k, int64_t u, Lookup& l) {
+  l.code = 0;
+  l.entry = -1;
+  l.dist = 0.f;
   if (u < k.n_w) {
     if (!p.x_chunk) {
-      dist = static_cast<float>((k.t - u) % p.n_win);  // slot u holds the latest position up to t that is u mod n_win
-      return (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + u);
+      l.dist = static_cast<float>((k.t - u) % p.n_win);  // slot u holds the latest position up to t that is u mod n_win
+      l.code = (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + u);
+      return;
     }
     const int64_t pos = k.ws + u;
-    dist = static_cast<float>(k.t - pos);
+    l.dist = static_cast<float>(k.t - pos);
     const int64_t cr = chunk_row(p, seq, pos);
-    if (cr >= 0) return (3u << kRowBits) | static_cast<uint32_t>(cr);
-    return (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + pos % p.n_win);
+    l.code = cr >= 0 ? (3u << kRowBits) | static_cast<uint32_t>(cr)
+                     : (2u << kRowBits) | static_cast<uint32_t>((int64_t)seq * p.n_win + pos % p.n_win);
+    return;
   }
   const int64_t jj = u - k.n_w;
-  const int64_t j = p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k + jj]) : jj;
-  if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return 0;
-  dist = entry_distance(k.t, j, p.m);
+  l.entry = p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k + jj]) : jj;
+}
+__device__ __forceinline__ void look_page(const AttendParams& p, int seq, const Keys& k, Lookup& l) {
+  l.page = -1;
+  const int64_t j = l.entry;
+  if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return;
+  l.dist = entry_distance(k.t, j, p.m);
   const int64_t pi = j / p.page_size;
-  if (pi >= p.max_pages_per_seq) return 0;
-  const int32_t page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
-  if (page < 0 || page >= p.n_pages) return 0;
-  return (1u << kRowBits) | static_cast<uint32_t>((int64_t)page * p.page_size + j % p.page_size);
+  if (pi < p.max_pages_per_seq) l.page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
+}
+__device__ __forceinline__ uint32_t look_row(const AttendParams& p, const Lookup& l) {
+  if (l.code) return l.code;
+  if (l.page < 0 || l.page >= p.n_pages) return 0;
+  return (1u << kRowBits) | static_cast<uint32_t>((int64_t)l.page * p.page_size + l.entry % p.page_size);
 }
 
 // the bf16 row of a code (an FP8 pool row is read as codes by the loaders)
@@ -208,11 +227,13 @@ __device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q,
 // FP8: the pool holds E4M3 entries with an fp32 scale each (a separate
 // instantiation keeps the bf16 kernel's code small)
 template <bool FP8, bool RULE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ring,
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvg,
                      const AttendParams p, const __grid_constant__ Rule rule) {
   using Sm = Smem<FP8, RULE>;
+  constexpr int kThreads = Block<FP8>::kThreads, kLoaders = Block<FP8>::kLoaders;
+  constexpr int kHalfPer = (kChunks + 2 * kLoaders - 1) / (2 * kLoaders);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Sm::Q;
@@ -297,6 +318,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t g = 0;       // tiles processed by this CTA before the current item
   uint32_t n_item = 0;  // items processed before the current one (qbar / dbar phase)
 
+  if constexpr (FP8) {  // 240 x 128 + 128 x 256 registers of the block's 168 x 384
+    if (warp < 4)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 240;\n");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 128;\n");
+  }
+
   // consecutive items are the head groups of one split, so the CTAs reading the same keys run together
   for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
     int lo = 0, hi = p.n_q - 1;
@@ -346,33 +374,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return -1;
       };
-      // the source row of key lt of tile it (threads 0 .. kNk - 1), and its FP8 scale
-      auto code_of = [&](int it, float& sc, float& di) -> uint32_t {
-        sc = 0.f;
-        di = 0.f;
+      // key lt of tile it (threads 0 .. kNk - 1)
+      auto key_at = [&](int it, Lookup& l) {
+        l.code = 0;
+        l.entry = -1;
+        l.dist = 0.f;
         const int i = it * kNk + lt;
-        if (lt >= kNk || i >= nk || !seq_ok) return 0u;
-        const uint32_t c = key_code(p, b, seq, kk, u0 + i, di);
-        if (!c) {
-          if (grp == 0) report(p.status, CSKV_ERR_OUT_OF_RANGE);
-          return 0u;
-        }
-        sc = (fp8 && (c >> kRowBits) == 1u) ? p.kv_scale[c & kRowMask] : 1.f;
-        return c;
+        if (lt < kNk && i < nk && seq_ok) look_key(p, b, seq, kk, u0 + i, l);
       };
-      auto prefetch = [&](uint32_t c) {  // the row into L2 ahead of its copy
+      // the row into L2 ahead of its copy, line by line (a bulk prefetch is issued for one lane at a time: ~70 cycles
+      // a row, 4,500 a tile)
+      auto prefetch = [&](uint32_t c) {
         if (!c) return;
-        if (fp8 && (c >> kRowBits) == 1u)
-          prefetch_l2(static_cast<const uint8_t*>(p.kv_pool) + (size_t)(c & kRowMask) * kDqk, kDqk);
-        else
-          prefetch_l2(code_row(p, c), kDqk * 2);
+        const bool codes = fp8 && (c >> kRowBits) == 1u;
+        const uint8_t* row = codes ? static_cast<const uint8_t*>(p.kv_pool) + (size_t)(c & kRowMask) * kDqk
+                                   : reinterpret_cast<const uint8_t*>(code_row(p, c));
+        for (int o = 0; o < (codes ? kDqk : 2 * kDqk); o += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row + o));
       };
-      // the next tile's source (its page-table lookup included) is found before its stage frees
+      // the next tile's source is found before its stage frees; its key two tiles, its page one tile before that
       float nsc = 0.f, ndist = 0.f;
-      uint32_t ncode = ntiles > 0 ? code_of(0, nsc, ndist) : 0u;
-      int nrow0 = 0;
-      int nmode = ntiles > 0 ? tile_src(0, nrow0) : -1;
-      if (ntiles > 0 && nmode < 0) prefetch(ncode);
+      uint32_t ncode = 0u;
+      int nrow0 = 0, nmode = -1;
+      Lookup l1, l2;  // of the tiles it + 1 (page found) and it + 2 (key found), seen from tile it
+      auto next = [&](int it) {  // the source of tile it + 1, and the lookups of the two after it a step further
+        ncode = look_row(p, l1);
+        ndist = l1.dist;
+        if (!ncode && lt < kNk && (it + 1) * kNk + lt < nk && seq_ok && grp == 0) report(p.status, CSKV_ERR_OUT_OF_RANGE);
+        nsc = !ncode ? 0.f : (fp8 && (ncode >> kRowBits) == 1u) ? p.kv_scale[ncode & kRowMask] : 1.f;
+        nmode = tile_src(it + 1, nrow0);
+        if (nmode < 0) prefetch(ncode);
+        l1 = l2;
+        look_page(p, seq, kk, l1);
+        key_at(it + 3, l2);
+      };
+      key_at(0, l1);
+      key_at(1, l2);
+      look_page(p, seq, kk, l1);
+      if (ntiles > 0) next(-1);
       for (int it = 0; it < ntiles; ++it) {
         const uint32_t gt = g + it;
         const int st = gt & 1;
@@ -414,11 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap* map = mode == 0 ? &tm_ring : &tm_kv;
             for (int j = 0; j < kNb; ++j) tma_load_2d(dst + j * kBlkBytes, map, j * 64, row0, &kfull[st]);
           }
-          if (it + 1 < ntiles) {
-            ncode = code_of(it + 1, nsc, ndist);
-            nmode = tile_src(it + 1, nrow0);
-            if (nmode < 0) prefetch(ncode);
-          }
+          if (it + 1 < ntiles) next(it);
         } else if (!fp8 && sPool[0] && sPool[1]) {
           // the tile's rows by TMA gather, four rows of one 64-channel block per copy; a key without
           // a row reads row -1, outside the map: zeros, as the copies below would write
@@ -434,11 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tma_gather4(dst + j * kBlkBytes + r4 * 128, &tm_kvg, j * 64, y[0], y[1], y[2], y[3], &kfull[st]);
           }
-          if (it + 1 < ntiles) {
-            ncode = code_of(it + 1, nsc, ndist);
-            nmode = tile_src(it + 1, nrow0);
-            if (nmode < 0) prefetch(ncode);
-          }
+          if (it + 1 < ntiles) next(it);
         } else if (fp8 && sPool[0] && sPool[1]) {
           // FP8 pool rows: the tile's E4M3 codes (half a bf16 tile) are copied into the stage's upper
           // half by cp.async, block-major (block j's 64 codes of every key at stg + 4096 j), so the
@@ -451,31 +481,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           static_assert(kStg + kNb * kCodeBlk == kStageBytes && 4 * kBlkBytes <= kStg, "staging");
           uint8_t* stg = dst + kStg;
           const uint8_t* pool = static_cast<const uint8_t*>(p.kv_pool);
+#pragma unroll 6
           for (int q = lt; q < kNk * kNb * 4; q += kLoaders) {  // (key, block, 16-byte piece)
             const int kr = q / (kNb * 4), j = (q / 4) % kNb, c4 = q % 4;
             const uint32_t cd = sCode[kr];
-            if (cd)
-              cp_async16(stg + j * kCodeBlk + kr * 64 + c4 * 16,
-                         pool + (size_t)(cd & kRowMask) * kDqk + j * 64 + c4 * 16, 16);
+            cp_async16(stg + j * kCodeBlk + kr * 64 + c4 * 16,
+                       cd ? pool + (size_t)(cd & kRowMask) * kDqk + j * 64 + c4 * 16 : pool, cd ? 16 : 0);
           }
           cp_async_commit();
-          if (it + 1 < ntiles) {  // the next tile's rows are looked up while the codes fly
-            ncode = code_of(it + 1, nsc, ndist);
-            nmode = tile_src(it + 1, nrow0);
-            if (nmode < 0) prefetch(ncode);
-          }
+          if (it + 1 < ntiles) next(it);  // the next tile's rows are looked up while the codes fly
           cp_async_wait<0>();
           // the 8 codes of bf16 chunk (key kr, block j, piece pc), and their widened store
           auto codes_at = [&](int kr, int j, int pc) -> uint2 {
-            return sCode[kr] ? *reinterpret_cast<const uint2*>(stg + j * kCodeBlk + kr * 64 + pc * 8)
-                                        : make_uint2(0u, 0u);
+            return *reinterpret_cast<const uint2*>(stg + j * kCodeBlk + kr * 64 + pc * 8);
           };
           auto put = [&](int kr, int j, int pc, uint2 c8) {
             *reinterpret_cast<uint4*>(dst + j * kBlkBytes + kr * 128 + ((pc ^ (kr & 7)) << 4)) = e4m3x8_to_bf16x8(c8);
           };
           auto widen = [&](int j0, int j1) {  // blocks j0 .. j1 - 1
+#pragma unroll 4
             for (int id = lt; id < kNk * (j1 - j0) * 8; id += kLoaders) {
-              const int kr = id / ((j1 - j0) * 8), j = j0 + (id / 8) % (j1 - j0), pc = id % 8;
+              const int kr = (id / 8) % kNk, j = j0 + id / (8 * kNk), pc = id % 8;
               put(kr, j, pc, codes_at(kr, j, pc));
             }
           };
@@ -506,13 +532,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // consecutive threads take consecutive 16-byte chunks of a row (coalesced): chunk c of key
           // kr is 16-byte piece c & 7 of channel block c >> 3; FP8 entries are read as 8 codes and
-          // widened, in passes of kPer / 2 chunks to bound the registers they hold
+          // widened, in two passes to bound the registers they hold
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            uint2 codes8[kPer / 2];
+            uint2 codes8[kHalfPer];
 #pragma unroll
-            for (int q = 0; q < kPer / 2; ++q) {
-              const int id = lt + (half * (kPer / 2) + q) * kLoaders;
+            for (int q = 0; q < kHalfPer; ++q) {
+              const int id = lt + (half * kHalfPer + q) * kLoaders;
               codes8[q] = make_uint2(0u, 0u);
               if (id < kChunks) {
                 const int kr = id / (kNb * 8), c = id % (kNb * 8);
@@ -530,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (fp8) {
 #pragma unroll
-              for (int q = 0; q < kPer / 2; ++q) {
-                const int id = lt + (half * (kPer / 2) + q) * kLoaders;
+              for (int q = 0; q < kHalfPer; ++q) {
+                const int id = lt + (half * kHalfPer + q) * kLoaders;
                 if (id < kChunks) {
                   const int kr = id / (kNb * 8), c = id % (kNb * 8);
                   if ((sCode[kr] >> kRowBits) == 1u)
@@ -542,11 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           cp_async_commit();
-          if (it + 1 < ntiles) {  // the next tile's rows are looked up while this tile's copies fly
-            ncode = code_of(it + 1, nsc, ndist);
-            nmode = tile_src(it + 1, nrow0);
-            if (nmode < 0) prefetch(ncode);
-          }
+          if (it + 1 < ntiles) next(it);  // the next tile's rows are looked up while this tile's copies fly
           cp_async_wait<0>();
           fence_proxy_async_smem();
           named_sync(3, kLoaders);
@@ -837,7 +859,7 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st) {
   const int64_t items = (int64_t)p.n_q * p.max_splits * (p.n_heads / kH);
   const int grid = static_cast<int>(items < n_sm ? items : n_sm);
   p.part_t = 1;
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(grid < 1 ? 1 : grid)), dim3(kThreads), smem, st, tm_q, tm_ring,
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(grid < 1 ? 1 : grid)), dim3(fp8 ? Block<true>::kThreads : Block<false>::kThreads), smem, st, tm_q, tm_ring,
                  tm_kv, tm_kvg, p, make_rule(p.sm_scale, p.score_cap));
   if (e != cudaSuccess) return e;
   return launch_attend_merge(p, st);
