@@ -20,6 +20,7 @@
 // and their per-entry scale is applied to the logits and to P. RULE is the form
 // with a cap or a distance bias on the logits: each key's distance stands beside
 // its row, and the rule is applied to the fp32 logit before the online softmax.
+#include "attend_plan.cuh"
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
   const int mt = warp % MT, vs = warp / MT;
   const int g = lane >> 2, c = lane & 3;
   const int n_groups = p.n_heads / HG;
-  const int kps = p.keys_per_split;
+  const int kps = RULE ? plan_split(p, KT, p.slots, lane, [&](int b) { return query_keys(p, b).n; }) : p.keys_per_split;
 
   // items per query: splits * head groups; exclusive prefix in shared memory
   {
@@ -150,6 +151,10 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
   if (blockIdx.x == 0)
     for (int b = tid; b < p.n_q; b += NTH)
       if (p.q_pos[b] < 0 || p.q_pos[b] > p.max_pos) report(p.status, CSKV_ERR_INVALID_ARG);
+  if (RULE && blockIdx.x == 0) {
+    if (tid == 0) p.plan[0] = kps;
+    for (int b = tid; b <= p.n_q; b += NTH) p.plan[1 + b] = sPref[b] / n_groups;
+  }
   const int total = sPref[p.n_q];
 
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
@@ -342,7 +347,8 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
       l_run[h] += __shfl_xor_sync(kFull, l_run[h], 2);
     }
     const int head0 = grp * HG + mt * 16 + g;
-    const int64_t prow0 = ((int64_t)b * p.max_splits + split) * p.n_heads + head0;
+    const int64_t slot = RULE ? sPref[b] / n_groups + split : (int64_t)b * p.max_splits + split;
+    const int64_t prow0 = slot * p.n_heads + head0;
     const int64_t prow1 = prow0 + 8;
     const float inv0 = l_run[0] > 0.f ? 1.f / l_run[0] : 0.f;
     const float inv1 = l_run[1] > 0.f ? 1.f / l_run[1] : 0.f;
@@ -360,18 +366,28 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
   }
 }
 
+// Query b's pieces: how many, and the first one's slot.
+__device__ __forceinline__ int pieces_of(const AttendParams& p, int b, int64_t& first) {
+  if (p.plan) {
+    first = p.plan[1 + b];
+    return p.plan[2 + b] - p.plan[1 + b];
+  }
+  first = (int64_t)b * p.max_splits;
+  return static_cast<int>((query_keys(p, b).n + p.keys_per_split - 1) / p.keys_per_split);
+}
+
 // out[b,h,:] = sum_s exp(lse_s - L) o_s,  L = log sum_s exp(lse_s)
 // d_v / 4 threads per head, four channels each; the split loop issues eight
 // independent loads at a time.
 __global__ void __launch_bounds__(256) attend_merge_kernel(AttendParams p) {
   const int b = blockIdx.x;
-  const QueryKeys qk = query_keys(p, b);
-  const int ns = static_cast<int>((qk.n + p.keys_per_split - 1) / p.keys_per_split);
+  int64_t first;
+  const int ns = pieces_of(p, b, first);
   const int hb = blockDim.x / (p.d_v / 4);  // heads per pass: d_v/4 threads per head
   const int hl = threadIdx.x / (p.d_v / 4);
   const int c4 = (threadIdx.x % (p.d_v / 4)) * 4;
   for (int h = blockIdx.y * hb + hl; h < p.n_heads && hl < hb; h += gridDim.y * hb) {
-    const int64_t base = (int64_t)b * p.max_splits * p.n_heads + h;
+    const int64_t base = first * p.n_heads + h;
     float L = -INFINITY;
     for (int s = 0; s < ns; ++s) L = fmaxf(L, p.part_lse[base + (int64_t)s * p.n_heads]);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -418,12 +434,12 @@ __global__ void __launch_bounds__(256) attend_merge_t_kernel(AttendParams p) {
   grid_dependency_wait();  // the partial outputs come from the attention kernel ahead of this one
   grid_dependents_launch();
   const int b = blockIdx.x;
-  const QueryKeys qk = query_keys(p, b);
-  const int ns = static_cast<int>((qk.n + p.keys_per_split - 1) / p.keys_per_split);
+  int64_t first;
+  const int ns = pieces_of(p, b, first);
   const int h = blockIdx.z * 128 + (threadIdx.x & 127);
   const int g4 = blockIdx.y * 2 + (threadIdx.x >> 7);  // group of 4 output channels
   if (h >= p.n_heads || g4 >= p.d_v / 4) return;
-  const int64_t lbase = (int64_t)b * p.max_splits * p.n_heads + h;
+  const int64_t lbase = first * p.n_heads + h;
   const float4* po = reinterpret_cast<const float4*>(p.part_o);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float wsum = 0.f;
@@ -438,7 +454,7 @@ __global__ void __launch_bounds__(256) attend_merge_t_kernel(AttendParams p) {
       o[s] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s < ns) {
         ls[s] = p.part_lse[lbase + (int64_t)s * p.n_heads];
-        o[s] = po[(((int64_t)b * p.max_splits + s) * (p.d_v / 4) + g4) * p.n_heads + h];
+        o[s] = po[((first + s) * (p.d_v / 4) + g4) * p.n_heads + h];
       }
     }
 #pragma unroll
@@ -467,7 +483,7 @@ __global__ void __launch_bounds__(256) attend_merge_t_kernel(AttendParams p) {
           o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (s < ns) {
             wg[j] = expf(p.part_lse[lbase + (int64_t)s * p.n_heads] - L);
-            o[j] = po[(((int64_t)b * p.max_splits + s) * (p.d_v / 4) + g4) * p.n_heads + h];
+            o[j] = po[((first + s) * (p.d_v / 4) + g4) * p.n_heads + h];
           }
         }
 #pragma unroll
@@ -508,6 +524,8 @@ cudaError_t run_attend_form(AttendParams& p, int n_sm, cudaStream_t st) {
   int64_t grid = (int64_t)n_sm * per_sm;
   if (grid > upper) grid = upper;
   if (grid < 1) grid = 1;
+  const int64_t want = (int64_t)n_sm * per_sm / groups, most = (int64_t)p.n_q * p.max_splits;
+  p.slots = static_cast<int>(want < most ? want : most);
   kern<<<static_cast<int>(grid), 32 * MT * VS, smem, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -573,7 +591,7 @@ static void choose_split(AttendParams& p, int n_sm) {
 
 static size_t plan_bytes(const AttendParams& p) {
   const size_t rows = (size_t)p.n_q * p.max_splits * p.n_heads;
-  return rows * p.d_v * sizeof(float) + rows * sizeof(float) + 256;
+  return rows * p.d_v * sizeof(float) + rows * sizeof(float) + sizeof(int32_t) * ((size_t)p.n_q + 2) + 256;
 }
 
 // The query takes no score rule, so it covers both forms: the larger of the plans where they differ.
@@ -599,6 +617,7 @@ cudaError_t launch_attend(AttendParams& p, void* ws, int n_sm, cudaStream_t st) 
   const size_t rows = (size_t)p.n_q * p.max_splits * p.n_heads;
   p.part_o = static_cast<float*>(ws);
   p.part_lse = p.part_o + rows * p.d_v;
+  p.plan = has_score_rule(p) ? reinterpret_cast<int32_t*>(p.part_lse + rows) : nullptr;
   if (p.n_q == 0) return cudaSuccess;
   if (attend_chunk_supported(p, n_sm)) return launch_attend_chunk(p, n_sm, st);
   if (attend_pair_supported(p, n_sm)) return launch_attend_pair(p, n_sm, st);

@@ -48,6 +48,7 @@
 // RULE is the form with a cap or a distance bias on the logits: the loaders write
 // each key's distance beside its source row, and the softmax applies the rule to
 // the fp32 logits before the running max.
+#include "attend_plan.cuh"
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   const int groups = p.n_heads / kH;
-  const int kps = p.keys_per_split;
+  int kps = p.keys_per_split;
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
   // outputs (the selection, new cache rows) are read only from here on
   grid_dependency_wait();
   grid_dependents_launch();
+  if constexpr (RULE) kps = plan_split(p, kNk, p.slots, lane, [&](int b) { return keys_of(p, b).n; });
   {  // items per query: splits x head groups
     int run = 0;
     for (int base = 0; base < p.n_q; base += kThreads) {
@@ -314,6 +316,10 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
   if (blockIdx.x == 0)
     for (int b = tid; b < p.n_q; b += kThreads)
       if (p.q_pos[b] < 0 || p.q_pos[b] > p.max_pos) report(p.status, CSKV_ERR_INVALID_ARG);
+  if (RULE && blockIdx.x == 0) {
+    if (tid == 0) p.plan[0] = kps;
+    for (int b = tid; b <= p.n_q; b += kThreads) p.plan[1 + b] = sPref[b] / groups;
+  }
   const int total = sPref[p.n_q];
   uint32_t g = 0;       // tiles processed by this CTA before the current item
   uint32_t n_item = 0;  // items processed before the current one (qbar / dbar phase)
@@ -336,6 +342,8 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
     const int r = item - sPref[b];
     const int grp = r % groups;
     const int split = r / groups;
+    // where the piece's partial output goes
+    const int64_t slot = RULE ? sPref[b] / groups + split : (int64_t)b * p.max_splits + split;
     const Keys kk = keys_of(p, b);
     const int seq = p.q_seq[b];
     const bool seq_ok = seq >= 0 && seq < p.n_seqs_layer;
@@ -757,7 +765,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
       // part_o is head-minor ([query x split][d_v / 4][heads][4]): the 16 lanes of a half-warp
       // write 16 consecutive heads, 256 contiguous bytes
       float4* po = reinterpret_cast<float4*>(p.part_o) +
-                   (((int64_t)b * p.max_splits + split) * (kDv / 4) + kh * 64) * p.n_heads + head;
+                   (slot * (kDv / 4) + kh * 64) * p.n_heads + head;
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {
         uint32_t orow[32];
@@ -774,7 +782,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
         }
       }
       if (kh == 0)
-        p.part_lse[((int64_t)b * p.max_splits + split) * p.n_heads + head] =
+        p.part_lse[slot * p.n_heads + head] =
             l_row > 0.f ? (m_used + log2f(l_row)) * kLn2 : -INFINITY;
     }
     g += ntiles;
@@ -856,7 +864,9 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int64_t items = (int64_t)p.n_q * p.max_splits * (p.n_heads / kH);
+  const int64_t groups = p.n_heads / kH;
+  const int64_t items = (int64_t)p.n_q * p.max_splits * groups;
+  p.slots = static_cast<int>(n_sm / groups < (int64_t)p.n_q * p.max_splits ? n_sm / groups : (int64_t)p.n_q * p.max_splits);
   const int grid = static_cast<int>(items < n_sm ? items : n_sm);
   p.part_t = 1;
   e = launch_pdl(kern, dim3(static_cast<unsigned>(grid < 1 ? 1 : grid)), dim3(fp8 ? Block<true>::kThreads : Block<false>::kThreads), smem, st, tm_q, tm_ring,

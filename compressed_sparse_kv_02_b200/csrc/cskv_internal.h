@@ -171,6 +171,8 @@ struct AttendParams {
   float* part_lse; // [n_q * max_splits * n_heads]
   int max_splits;
   int keys_per_split;
+  int32_t* plan;   // with a score rule: keys per piece | first piece of each query [n_q + 1] (found by the kernel), or null
+  int slots;       // pieces it aims at
 };
 
 size_t attend_ws_bytes(const AttendParams& p, int n_sm);
