@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
   uint64_t* obar = bars + 8;          //     a tile's P V done (commit)
   uint64_t* qbar = bars + 9;          //     Q of the item landed (TMA)
   uint64_t* dbar = bars + 10;         //     the item's last P V done (commit)
+  uint64_t* cbar = bars + 11;         //     a tile's FP8 codes landed (TMA)
   constexpr bool fp8 = FP8;
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Sm::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Sm::FLAGS);
@@ -274,6 +275,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
     mbar_init(obar, 1);
     mbar_init(qbar, 1);
     mbar_init(dbar, 1);
+    mbar_init(cbar, 1);
     fence_barrier_init();
     *sAbort = 0;
   }
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_ring);
     prefetch_tensormap(&tm_kv);
-    if (!FP8) prefetch_tensormap(&tm_kvg);
+    prefetch_tensormap(&tm_kvg);
   }
   if (warp == 4) {
     tmem_alloc(sTmem, kTmemCols);
@@ -323,6 +325,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
   const int total = sPref[p.n_q];
   uint32_t g = 0;       // tiles processed by this CTA before the current item
   uint32_t n_item = 0;  // items processed before the current one (qbar / dbar phase)
+  uint32_t n_gather = 0;  // FP8 tiles gathered (cbar phase)
 
   if constexpr (FP8) {  // 240 x 128 + 128 x 256 registers of the block's 168 x 384
     if (warp < 4)
@@ -478,30 +481,37 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
           }
           if (it + 1 < ntiles) next(it);
         } else if (fp8 && sPool[0] && sPool[1]) {
-          // FP8 pool rows: the tile's E4M3 codes (half a bf16 tile) are copied into the stage's upper
-          // half by cp.async, block-major (block j's 64 codes of every key at stg + 4096 j), so the
-          // next tile's row lookups overlap the copies; then they are widened exactly to bf16 in
-          // place, in passes whose writes cover only staged blocks that earlier passes have read:
-          // blocks 0-3 (below the staged codes), 4-5, 6, 7, then 8, whose own codes it overwrites
-          // (read first, then a barrier). A key without a row gets zeros.
-          constexpr int kStg = kStageBytes / 2;            // 36864
-          constexpr int kCodeBlk = kNk * 64;               // 4096: one staged block of codes
-          static_assert(kStg + kNb * kCodeBlk == kStageBytes && 4 * kBlkBytes <= kStg, "staging");
-          uint8_t* stg = dst + kStg;
-          const uint8_t* pool = static_cast<const uint8_t*>(p.kv_pool);
-#pragma unroll 6
-          for (int q = lt; q < kNk * kNb * 4; q += kLoaders) {  // (key, block, 16-byte piece)
-            const int kr = q / (kNb * 4), j = (q / 4) % kNb, c4 = q % 4;
-            const uint32_t cd = sCode[kr];
-            cp_async16(stg + j * kCodeBlk + kr * 64 + c4 * 16,
-                       cd ? pool + (size_t)(cd & kRowMask) * kDqk + j * 64 + c4 * 16 : pool, cd ? 16 : 0);
+          // FP8 pool rows: TMA gathers the tile's E4M3 codes, four rows of 128 channels per copy (a missing row
+          // reads zeros), into five pieces of 64 swizzled 128-byte rows over the stage's last 40 KB; the rows are
+          // spread over the whole pool, and copies by the threads (cp.async) stood in line for their translations
+          // (4,400 cycles a tile). The codes are then widened exactly to bf16 in place: block j's 8 KB start at
+          // 8192 j, so block 4 + i overwrites piece i, which holds blocks 2i and 2i + 1: blocks 0-3 (below the
+          // pieces) first, then 4 and 5, then 6; 7 and 8 lie in the pieces they overwrite and are read before.
+          constexpr int kStg = 4 * kBlkBytes;
+          constexpr int kPieces = (kDqk + 127) / 128;
+          static_assert(kStg + kPieces * kBlkBytes == kStageBytes, "staging");
+          const uint8_t* stg = dst + kStg;
+          if (lt == 0) mbar_arrive_expect_tx(cbar, kPieces * kBlkBytes);
+          named_sync(3, kLoaders);  // the byte count is set before any of the copies lands
+          const int q = (lt & 31) * (kLoaders / 32) + (lt >> 5);  // spread over the warps: each issues one lane at a time
+          if (q < kPieces * (kNk / 4)) {
+            const int j = q / (kNk / 4), r4 = (q % (kNk / 4)) * 4;
+            int y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t cd = sCode[r4 + e];
+              y[e] = (cd >> kRowBits) == 1u ? static_cast<int>(cd & kRowMask) : -1;
+            }
+            tma_gather4(dst + kStg + j * kBlkBytes + r4 * 128, &tm_kvg, j * 128, y[0], y[1], y[2], y[3], cbar);
           }
-          cp_async_commit();
+          __syncwarp();
           if (it + 1 < ntiles) next(it);  // the next tile's rows are looked up while the codes fly
-          cp_async_wait<0>();
+          const bool landed = __all_sync(kFull, mbar_wait(cbar, n_gather & 1u, p.status));
+          ++n_gather;
           // the 8 codes of bf16 chunk (key kr, block j, piece pc), and their widened store
           auto codes_at = [&](int kr, int j, int pc) -> uint2 {
-            return *reinterpret_cast<const uint2*>(stg + j * kCodeBlk + kr * 64 + pc * 8);
+            const int c16 = ((j & 1) * 4 + (pc >> 1)) ^ (kr & 7);
+            return *reinterpret_cast<const uint2*>(stg + (j >> 1) * kBlkBytes + kr * 128 + c16 * 16 + (pc & 1) * 8);
           };
           auto put = [&](int kr, int j, int pc, uint2 c8) {
             *reinterpret_cast<uint4*>(dst + j * kBlkBytes + kr * 128 + ((pc ^ (kr & 7)) << 4)) = e4m3x8_to_bf16x8(c8);
@@ -513,26 +523,26 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
               put(kr, j, pc, codes_at(kr, j, pc));
             }
           };
-          named_sync(3, kLoaders);  // every staged code is visible to every loader
           widen(0, 4);
+          if (named_sync_or(3, kLoaders, !landed)) {
+            *sAbort = 1;
+            break;
+          }
+          widen(4, 6);
           named_sync(3, kLoaders);
-          widen(4, 6);  // overwrites staged blocks 0-2
-          named_sync(3, kLoaders);
-          widen(6, 7);  // 3-4
-          named_sync(3, kLoaders);
-          widen(7, 8);  // 5-6
-          constexpr int kLastPer = (kNk * 8 + kLoaders - 1) / kLoaders;  // 6
+          widen(6, 7);
+          constexpr int kLastPer = (2 * kNk * 8 + kLoaders - 1) / kLoaders;  // 5
           uint2 last[kLastPer];
 #pragma unroll
           for (int k2 = 0; k2 < kLastPer; ++k2) {
             const int id = lt + k2 * kLoaders;
-            last[k2] = id < kNk * 8 ? codes_at(id / 8, kNb - 1, id % 8) : make_uint2(0u, 0u);
+            last[k2] = id < 2 * kNk * 8 ? codes_at((id / 8) % kNk, 7 + id / (8 * kNk), id % 8) : make_uint2(0u, 0u);
           }
-          named_sync(3, kLoaders);  // block 8 overwrites staged blocks 7-8, read by now
+          named_sync(3, kLoaders);
 #pragma unroll
           for (int k2 = 0; k2 < kLastPer; ++k2) {
             const int id = lt + k2 * kLoaders;
-            if (id < kNk * 8) put(id / 8, kNb - 1, id % 8, last[k2]);
+            if (id < 2 * kNk * 8) put((id / 8) % kNk, 7 + id / (8 * kNk), id % 8, last[k2]);
           }
           fence_proxy_async_smem();
           named_sync(3, kLoaders);
@@ -812,6 +822,19 @@ bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// rows of E4M3 codes in one-row boxes of 128 channels (the last box reaches past the row: zeros)
+bool encode_codes(CUtensorMap* map, const void* base, uint64_t rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kDqk), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kDqk)};
+  const cuuint32_t box[2] = {128, 1};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace
 
 static size_t smem_bytes(bool fp8, bool rule, int n_q) {
@@ -850,12 +873,12 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st) {
     return cudaErrorNotSupported;
   if (!encode_rows(&tm_q, p.q, static_cast<uint64_t>(p.n_q) * p.n_heads, kH) ||
       !encode_rows(&tm_ring, p.ring_x, ring_rows, kNk) ||
-      // an FP8 pool is never read by TMA (its tiles are widened by the loaders)
+      // FP8 entries are gathered as codes, never copied as bf16 rows
       !encode_rows(&tm_kv, p.kv_dtype == CSKV_FP8_E4M3 ? static_cast<const void*>(p.ring_x) : p.kv_pool,
                    p.kv_dtype == CSKV_FP8_E4M3 ? ring_rows : kv_rows, kNk) ||
-      // one-row boxes of the bf16 pool for the gathered tiles (the selection's rows)
-      !encode_rows(&tm_kvg, p.kv_dtype == CSKV_FP8_E4M3 ? static_cast<const void*>(p.ring_x) : p.kv_pool,
-                   p.kv_dtype == CSKV_FP8_E4M3 ? ring_rows : kv_rows, 1))
+      // one-row boxes of the pool for the gathered tiles (the selection's rows, every FP8 entry)
+      !(p.kv_dtype == CSKV_FP8_E4M3 ? encode_codes(&tm_kvg, p.kv_pool, kv_rows)
+                                    : encode_rows(&tm_kvg, p.kv_pool, kv_rows, 1)))
     return cudaErrorNotSupported;
   const bool fp8 = p.kv_dtype == CSKV_FP8_E4M3, rule = has_score_rule(p);
   const size_t smem = smem_bytes(fp8, rule, p.n_q);
