@@ -111,6 +111,7 @@ struct Keys {
   int64_t t, ws;
   int n_w;
   int64_t n;
+  int64_t n_vis;  // entries visible at t
 };
 
 __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
@@ -119,15 +120,14 @@ __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
   r.ws = 0;
   r.n_w = 0;
   r.n = 0;
+  r.n_vis = 0;
   if (r.t < 0 || r.t > p.max_pos) return r;
   r.ws = window_start(r.t, p.n_win);
   r.n_w = static_cast<int>(r.t - r.ws + 1);
-  int64_t n_c;
+  int64_t n_c = r.n_vis = visible_entries(r.t, p.m, p.n_win);
   if (p.is_csa) {
     const int64_t c = p.sel_cnt[b];
     n_c = c < 0 ? 0 : (c > p.k ? p.k : c);
-  } else {
-    n_c = visible_entries(r.t, p.m, p.n_win);
   }
   r.n = r.n_w + n_c;
   return r;
@@ -140,6 +140,7 @@ __device__ __forceinline__ Keys keys_of(const AttendParams& p, int b) {
 struct Lookup {
   uint32_t code;  // of a window row
   int32_t page;   // of an entry's
+  int32_t slot;   // its place in the page
   int64_t entry;  // the entry, -1: none
   float dist;     // the key's distance from the query in tokens (RULE)
 };
@@ -166,15 +167,16 @@ __device__ __forceinline__ void look_key(const AttendParams& p, int b, int seq, 
 __device__ __forceinline__ void look_page(const AttendParams& p, int seq, const Keys& k, Lookup& l) {
   l.page = -1;
   const int64_t j = l.entry;
-  if (j < 0 || j >= visible_entries(k.t, p.m, p.n_win)) return;
+  if (j < 0 || j >= k.n_vis) return;
   l.dist = entry_distance(k.t, j, p.m);
-  const int64_t pi = j / p.page_size;
+  const int64_t pi = j < 0x7fffffff ? static_cast<uint32_t>(j) / static_cast<uint32_t>(p.page_size) : j / p.page_size;
+  l.slot = static_cast<int32_t>(j - pi * p.page_size);
   if (pi < p.max_pages_per_seq) l.page = p.page_table[(int64_t)seq * p.max_pages_per_seq + pi];
 }
 __device__ __forceinline__ uint32_t look_row(const AttendParams& p, const Lookup& l) {
   if (l.code) return l.code;
   if (l.page < 0 || l.page >= p.n_pages) return 0;
-  return (1u << kRowBits) | static_cast<uint32_t>((int64_t)l.page * p.page_size + l.entry % p.page_size);
+  return (1u << kRowBits) | static_cast<uint32_t>((int64_t)l.page * p.page_size + l.slot);
 }
 
 // the bf16 row of a code (an FP8 pool row is read as codes by the loaders)
