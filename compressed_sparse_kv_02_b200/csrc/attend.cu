@@ -436,6 +436,7 @@ __global__ void __launch_bounds__(256) attend_merge_t_kernel(AttendParams p) {
   const int b = blockIdx.x;
   int64_t first;
   const int ns = pieces_of(p, b, first);
+  if (p.plan && ns == 1 && p.rope_dims == 0) return;  // written by the attention kernel
   const int h = blockIdx.z * 128 + (threadIdx.x & 127);
   const int g4 = blockIdx.y * 2 + (threadIdx.x >> 7);  // group of 4 output channels
   if (h >= p.n_heads || g4 >= p.d_v / 4) return;

@@ -28,9 +28,8 @@
 //     keys, and the row max is one more swap; the two lanes of a row keep the
 //     same running max, and the rare O rescale touches exactly the O rows of
 //     every lane (both halves);
-//   - one warp issues only S, so the next tile's S runs while this tile's
-//     exponentials are taken; softmax thread 0 issues the tile's P V once every
-//     row has stored its P (a named barrier that also decides aborts uniformly);
+//   - one warp issues S and P V, so the next tile's S runs while this tile's
+//     exponentials are taken;
 //   - loaders look up each tile's source rows one tile ahead, while the tile
 //     before it is copied (its page-table reads included): TMA when a
 //     tile's rows are contiguous (window rows of the ring, HCA entries of one
@@ -64,14 +63,18 @@ constexpr int kStageBytes = kNb * kBlkBytes;    // 73728: a key tile (also the Q
 constexpr int kNS = 2;                          // key-tile stages
 constexpr int kPBytes = kH * kNk * 2;           // 8192: P of the tile (bf16)
 constexpr int kLoadThread0 = 160;               // warps 0-3 softmax, warp 4 S, then the loaders
-// Loader warps: three for bf16 entries; seven for FP8, whose widening to bf16 is what such a tile's time goes to (three
-// took MIXED3 us for the mixed workload's selection, seven MIXED7), with registers moved to the softmax warps.
+// Three loader warps. FP8 entries have eight more that copy the codes of a tile and widen them to bf16, eight keys each,
+// while the loaders look up the next one.
+constexpr int kLoaders = 96;
+constexpr int kWidenThread0 = 256, kWideners = 256;
 template <bool FP8>
 struct Block {
-  static constexpr int kThreads = FP8 ? 384 : 256;
-  static constexpr int kLoaders = kThreads - kLoadThread0;  // 96 or 224
+  static constexpr int kThreads = FP8 ? kWidenThread0 + kWideners : 256;
 };
 constexpr int kChunks = kNk * kNb * 8;          // 16-byte chunks of a bf16 tile (4608)
+// an FP8 tile's codes: pieces of 128 channels behind the stage's first four blocks
+constexpr int kPieces = (kDqk + 127) / 128, kCodes0 = 4 * kBlkBytes;
+static_assert(kCodes0 + kPieces * kBlkBytes == kStageBytes, "code pieces");
 constexpr uint32_t kTmemCols = 512;
 // O[:, 0:256] lanes +0 and O[:, 256:512] lanes +16 of columns 0-255; S buffer k at columns
 // 256 + 64 k (even channel blocks at lanes +0, odd ones at lanes +16)
@@ -95,13 +98,15 @@ struct Smem {
   static constexpr int DIST = SCALE + (FP8 ? kNS * kNk * 4 : 0);  // RULE: [kNS][kNk] minus the distance of each key
   static constexpr int MASK = DIST + (RULE || !FP8 ? kNS * kNk * 4 : 0);  // [kNS][2] valid-key bits
   static constexpr int BAR = MASK + 32;                // mbarriers
-  static constexpr int TMEM = BAR + 16 * 8;            // allocated tensor-memory address
+  static constexpr int TMEM = BAR + 16 * 8;            // allocated tensor-memory address | FP8: tile kinds
   static constexpr int FLAGS = TMEM + 16;
   static constexpr int PREF = FLAGS + 16;              // [n_q + 1] items per query, exclusive prefix
   static size_t bytes(int n_q) { return 1024 + PREF + sizeof(int) * (size_t)(n_q + 1); }
 };
 
-static_assert(Smem<false, true>::DIST % 16 == 0 && Smem<true, true>::DIST % 16 == 0, "alignment");
+static_assert(Smem<false, true>::DIST % 16 == 0 && Smem<true, true>::DIST % 16 == 0 && Smem<true, true>::SCALE % 16 == 0 &&
+                  Smem<true, false>::SCALE % 16 == 0,
+              "alignment");
 
 // source-row code: kind in bits [31:30] (0 none, 1 pool entry, 2 ring row, 3 chunk row), row below
 constexpr uint32_t kRowBits = 30;
@@ -188,34 +193,53 @@ __device__ __forceinline__ const uint16_t* code_row(const AttendParams& p, uint3
   return nullptr;
 }
 
-// 8 E4M3 codes -> 8 bf16 (exact: every E4M3 value is a bf16 value)
+// 4 E4M3 codes -> 4 bf16, exact: every E4M3 value is a bf16 value. A code's four exponent and three mantissa bits, put
+// at the bottom of the exponent and the top of the mantissa of a bf16, stand for the value times 2^-120 (subnormals
+// included), so one packed product per two codes is left. The two codes that are NaN (all seven bits set) have no such
+// product: nan_codes finds them and set_nan writes them.
+__device__ __forceinline__ uint2 code_bits(uint32_t w) {
+  const uint32_t lo = (w << 4) & 0xf0f0f0f0u, hi = ((w >> 4) & 0x07070707u) | (w & 0x80808080u);  // the halves' bytes
+  return make_uint2(__byte_perm(lo, hi, 0x5140u), __byte_perm(lo, hi, 0x7362u));
+}
+__device__ __forceinline__ uint32_t unscale(uint32_t v) {
+  const uint32_t scale = 0x7b807b80u;  // 2^120 twice
+  const __nv_bfloat162 f = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&scale));
+  return *reinterpret_cast<const uint32_t*>(&f);
+}
+__device__ __forceinline__ uint4 widen8(uint2 c) {
+  const uint2 a = code_bits(c.x), b = code_bits(c.y);
+  return make_uint4(unscale(a.x), unscale(a.y), unscale(b.x), unscale(b.y));
+}
+__device__ __forceinline__ uint32_t nan_bits(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+// bit 7 of a byte: some code there is NaN
+__device__ __forceinline__ uint32_t nan_codes(uint2 c) { return (nan_bits(c.x) | nan_bits(c.y)) & 0x80808080u; }
+__device__ __forceinline__ uint4 set_nan(uint4 v, uint2 c) {
+  const uint2 a = code_bits(c.x), b = code_bits(c.y);
+  auto nan = [](uint32_t h) { return ((((h & 0x07f007f0u) + 0x00100010u) >> 11) & 0x00010001u) * 0x7fffu; };
+  return make_uint4(v.x | nan(a.x), v.y | nan(a.y), v.z | nan(b.x), v.w | nan(b.y));
+}
 __device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 c) {
-  uint32_t o[4];
-  const uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_fp8x2_storage_t v = static_cast<__nv_fp8x2_storage_t>((w[i >> 1] >> (16 * (i & 1))) & 0xffffu);
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3)));
-    o[i] = pack_bf16(f.x, f.y);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+  const uint4 v = widen8(c);
+  return nan_codes(c) ? set_nan(v, c) : v;
 }
 
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory");
 }
 // S of one key tile: 9 channel blocks x 4 K-steps (M = 64 heads, N = 64 keys); even blocks
-// accumulate at d (lanes +0), odd blocks at d + 16 lanes, the two chains issued alternately
+// accumulate at d (lanes +0), odd blocks at d + 16 lanes, the two chains issued alternately.
+// The stage is a uniform value, not a branch: every copy of this code is fetched cold once a block.
 __device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q, uint32_t k, uint32_t idesc) {
+  const uint64_t qd = umma_desc_sw128(q, 16, 1024), kd = umma_desc_sw128(k, 16, 1024);
 #pragma unroll
-  for (int s = 0; s < 20; ++s) {
-    const int ia = 2 * (s >> 2), ks = s & 3;
-    umma_ss_if(issuer, d, umma_desc_sw128(q + ia * kBlkBytes + ks * 32, 16, 1024),
-               umma_desc_sw128(k + ia * kBlkBytes + ks * 32, 16, 1024), idesc, s > 0 ? 1u : 0u);
-    if (s < 16) {
-      const int ib = ia + 1;
-      umma_ss_if(issuer, d + kLane16, umma_desc_sw128(q + ib * kBlkBytes + ks * 32, 16, 1024),
-                 umma_desc_sw128(k + ib * kBlkBytes + ks * 32, 16, 1024), idesc, s > 0 ? 1u : 0u);
+  for (int ia = 0; ia < kNb; ia += 2) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {  // a descriptor counts addresses in 16 bytes
+      const int o = ia * (kBlkBytes / 16) + 2 * ks;
+      umma_ss_if(issuer, d, qd + o, kd + o, idesc, o > 0 ? 1u : 0u);
+      if (ia + 1 < kNb)
+        umma_ss_if(issuer, d + kLane16, qd + kBlkBytes / 16 + o, kd + kBlkBytes / 16 + o, idesc, o > 0 ? 1u : 0u);
     }
   }
 }
@@ -223,10 +247,11 @@ __device__ __forceinline__ void issue_s(uint32_t issuer, uint32_t d, uint32_t q,
 // Pipeline (per CTA; tiles numbered gt across its items; stage and S buffer gt & 1):
 //   loaders : look up the tile's source rows -> wait kempty (P V of tile gt - 2 done) ->
 //             TMA, or cp.async / widened FP8 stores, into the stage -> kfull
-//   S warp  : wait kfull, sfree (softmax has read S(gt - 2)) -> S(gt) -> commit sfull
+//   MMA warp: kfull, sfree (softmax has read S(gt - 2)) -> S(gt) -> commit sfull;
+//             pfull -> P V(gt) -> commit kempty, obar
 //   softmax : wait sfull -> read S, swap halves with lane ^ 16, arrive sfree -> P(gt) ->
 //             wait obar (P V of gt - 1 done: P buffer free, O settled; rare rescale) ->
-//             store P -> named barrier -> thread 0: O += P V(gt) -> commit kempty, obar
+//             store P -> pfull
 // FP8: the pool holds E4M3 entries with an fp32 scale each (a separate
 // instantiation keeps the bf16 kernel's code small)
 template <bool FP8, bool RULE>
@@ -235,8 +260,9 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_kvg,
                      const AttendParams p, const __grid_constant__ Rule rule) {
   using Sm = Smem<FP8, RULE>;
-  constexpr int kThreads = Block<FP8>::kThreads, kLoaders = Block<FP8>::kLoaders;
-  constexpr int kHalfPer = (kChunks + 2 * kLoaders - 1) / (2 * kLoaders);
+  constexpr int kThreads = Block<FP8>::kThreads;
+  constexpr int kPasses = FP8 ? 6 : 2, kPer = kChunks / (kPasses * kLoaders);
+  static_assert(kPer * kPasses * kLoaders == kChunks, "chunks per pass");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Sm::Q;
@@ -247,19 +273,23 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
   float* sDist = reinterpret_cast<float*>(sm + Sm::DIST);
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Sm::MASK);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sm::BAR);
-  uint64_t* kfull = bars;             // [2] loaders -> S warp (and the softmax, for the stage's key bits)
+  uint64_t* kfull = bars;             // [2] loaders (and wideners) -> MMA warp (and the softmax, for the stage's key bits)
   uint64_t* kempty = bars + 2;        // [2] P V of the stage's tile done (commit)
   uint64_t* sfull = bars + 4;         // [2] S of the buffer's tile done (commit)
   uint64_t* sfree = bars + 6;         // [2] softmax has read the buffer (128 arrivals)
   uint64_t* obar = bars + 8;          //     a tile's P V done (commit)
   uint64_t* qbar = bars + 9;          //     Q of the item landed (TMA)
   uint64_t* dbar = bars + 10;         //     the item's last P V done (commit)
-  uint64_t* cbar = bars + 11;         //     a tile's FP8 codes landed (TMA)
+  uint64_t* rdy = bars + 11;          // [2] FP8, loaders -> wideners: the tile's kind and source rows are known
+  uint64_t* cfree = bars + 13;        //     FP8, wideners -> loaders: they have read the tile's source rows
+  uint64_t* cbar = bars + 14;         //     FP8: a tile's codes landed (TMA)
+  uint64_t* pfull = bars + 15;        //     softmax -> MMA warp: P of a tile is stored (128 arrivals)
   constexpr bool fp8 = FP8;
   uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + Sm::TMEM);
   volatile int* sAbort = reinterpret_cast<int*>(sm + Sm::FLAGS);
   volatile int* sLdOk = reinterpret_cast<int*>(sm + Sm::FLAGS) + 1;
   volatile int* sPool = reinterpret_cast<int*>(sm + Sm::FLAGS) + 2;  // [2] per code warp: the tile is gatherable
+  volatile int* sKind = reinterpret_cast<int*>(sm + Sm::TMEM) + 1;  // [2] FP8: the stage's tile is one of codes
   int* sPref = reinterpret_cast<int*>(sm + Sm::PREF);
   __shared__ int s_wsum[32];
 
@@ -269,15 +299,18 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&kfull[i], 1);
+      mbar_init(&kfull[i], FP8 ? 1 + kWideners / 32 : 1);
       mbar_init(&kempty[i], 1);
       mbar_init(&sfull[i], 1);
       mbar_init(&sfree[i], 128);
+      mbar_init(&rdy[i], 1);
     }
     mbar_init(obar, 1);
     mbar_init(qbar, 1);
     mbar_init(dbar, 1);
-    mbar_init(cbar, 1);
+    mbar_init(pfull, 128);
+    mbar_init(cfree, kWideners / 32);
+    mbar_init(cbar, kWideners / 32);
     fence_barrier_init();
     *sAbort = 0;
   }
@@ -327,14 +360,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
   const int total = sPref[p.n_q];
   uint32_t g = 0;       // tiles processed by this CTA before the current item
   uint32_t n_item = 0;  // items processed before the current one (qbar / dbar phase)
-  uint32_t n_gather = 0;  // FP8 tiles gathered (cbar phase)
-
-  if constexpr (FP8) {  // 240 x 128 + 128 x 256 registers of the block's 168 x 384
-    if (warp < 4)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 240;\n");
-    else
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 128;\n");
-  }
+  uint32_t n_gather = 0;  // FP8 tiles of codes before the current one (cbar phase)
 
   // consecutive items are the head groups of one split, so the CTAs reading the same keys run together
   for (int item = blockIdx.x; item < total; item += gridDim.x, ++n_item) {
@@ -357,10 +383,10 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
     const int ntiles = (nk + kNk - 1) / kNk;
     if (tid == 0 && grp == 0 && !seq_ok && kk.n > 0) report(p.status, CSKV_ERR_OUT_OF_RANGE);
 
-    if (tid >= kLoadThread0) {
+    if (tid >= kLoadThread0 && tid < kWidenThread0) {
       // ------------------------------------------------------------ loaders
       const int lt = tid - kLoadThread0, lw = lt >> 5, ll = lt & 31;
-      if (lw == 0) {  // Q of the head group: 9 boxes of 64 rows x 64 channels
+      if (lw == 2) {  // Q of the head group: 9 boxes of 64 rows x 64 channels (by the warp without lookups)
         if (ll == 0) {
           mbar_arrive_expect_tx(qbar, kStageBytes);
           const int qrow = b * p.n_heads + grp * kH;
@@ -395,14 +421,12 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
         const int i = it * kNk + lt;
         if (lt < kNk && i < nk && seq_ok) look_key(p, b, seq, kk, u0 + i, l);
       };
-      // the row into L2 ahead of its copy, line by line (a bulk prefetch is issued for one lane at a time: ~70 cycles
-      // a row, 4,500 a tile)
+      // the bf16 row into L2 ahead of its copy, line by line (a bulk prefetch is issued for one lane at a time: ~70
+      // cycles a row, 4,500 a tile)
       auto prefetch = [&](uint32_t c) {
         if (!c) return;
-        const bool codes = fp8 && (c >> kRowBits) == 1u;
-        const uint8_t* row = codes ? static_cast<const uint8_t*>(p.kv_pool) + (size_t)(c & kRowMask) * kDqk
-                                   : reinterpret_cast<const uint8_t*>(code_row(p, c));
-        for (int o = 0; o < (codes ? kDqk : 2 * kDqk); o += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row + o));
+        const uint8_t* row = reinterpret_cast<const uint8_t*>(code_row(p, c));
+        for (int o = 0; o < 2 * kDqk; o += 128) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row + o));
       };
       // the next tile's source is found before its stage frees; its key two tiles, its page one tile before that
       float nsc = 0.f, ndist = 0.f;
@@ -415,7 +439,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
         if (!ncode && lt < kNk && (it + 1) * kNk + lt < nk && seq_ok && grp == 0) report(p.status, CSKV_ERR_OUT_OF_RANGE);
         nsc = !ncode ? 0.f : (fp8 && (ncode >> kRowBits) == 1u) ? p.kv_scale[ncode & kRowMask] : 1.f;
         nmode = tile_src(it + 1, nrow0);
-        if (nmode < 0) prefetch(ncode);
+        if (nmode < 0 && !fp8) prefetch(ncode);  // a line of FP8 rows is gathered well before it is needed
         l1 = l2;
         look_page(p, seq, kk, l1);
         key_at(it + 3, l2);
@@ -434,6 +458,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
         if (lw == 0) {
           bool okw = __shfl_sync(kFull, *sAbort, 0) == 0;
           if (okw && gt >= 2u) okw = __all_sync(kFull, mbar_wait(&kempty[st], ((gt >> 1) - 1) & 1u, p.status));
+          if (FP8 && okw && gt >= 1u) okw = __all_sync(kFull, mbar_wait(cfree, (gt - 1) & 1u, p.status));
           if (ll == 0) *sLdOk = okw;
         }
         named_sync(3, kLoaders);
@@ -457,6 +482,11 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
         }
         named_sync(3, kLoaders);
         uint8_t* dst = sK + st * kStageBytes;
+        const bool pool = sPool[0] && sPool[1];
+        if (FP8 && lt == 0) {
+          sKind[st] = nmode < 0 && pool;
+          mbar_arrive(&rdy[st]);
+        }
         const int row0 = nrow0;
         const int mode = nmode;
         if (mode >= 0) {
@@ -466,7 +496,7 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
             for (int j = 0; j < kNb; ++j) tma_load_2d(dst + j * kBlkBytes, map, j * 64, row0, &kfull[st]);
           }
           if (it + 1 < ntiles) next(it);
-        } else if (!fp8 && sPool[0] && sPool[1]) {
+        } else if (!fp8 && pool) {
           // the tile's rows by TMA gather, four rows of one 64-channel block per copy; a key without
           // a row reads row -1, outside the map: zeros, as the copies below would write
           if (lt == 0) mbar_arrive_expect_tx(&kfull[st], kStageBytes);
@@ -482,85 +512,21 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
             tma_gather4(dst + j * kBlkBytes + r4 * 128, &tm_kvg, j * 64, y[0], y[1], y[2], y[3], &kfull[st]);
           }
           if (it + 1 < ntiles) next(it);
-        } else if (fp8 && sPool[0] && sPool[1]) {
-          // FP8 pool rows: TMA gathers the tile's E4M3 codes, four rows of 128 channels per copy (a missing row
-          // reads zeros), into five pieces of 64 swizzled 128-byte rows over the stage's last 40 KB; the rows are
-          // spread over the whole pool, and copies by the threads (cp.async) stood in line for their translations
-          // (4,400 cycles a tile). The codes are then widened exactly to bf16 in place: block j's 8 KB start at
-          // 8192 j, so block 4 + i overwrites piece i, which holds blocks 2i and 2i + 1: blocks 0-3 (below the
-          // pieces) first, then 4 and 5, then 6; 7 and 8 lie in the pieces they overwrite and are read before.
-          constexpr int kStg = 4 * kBlkBytes;
-          constexpr int kPieces = (kDqk + 127) / 128;
-          static_assert(kStg + kPieces * kBlkBytes == kStageBytes, "staging");
-          const uint8_t* stg = dst + kStg;
-          if (lt == 0) mbar_arrive_expect_tx(cbar, kPieces * kBlkBytes);
-          named_sync(3, kLoaders);  // the byte count is set before any of the copies lands
-          const int q = (lt & 31) * (kLoaders / 32) + (lt >> 5);  // spread over the warps: each issues one lane at a time
-          if (q < kPieces * (kNk / 4)) {
-            const int j = q / (kNk / 4), r4 = (q % (kNk / 4)) * 4;
-            int y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t cd = sCode[r4 + e];
-              y[e] = (cd >> kRowBits) == 1u ? static_cast<int>(cd & kRowMask) : -1;
-            }
-            tma_gather4(dst + kStg + j * kBlkBytes + r4 * 128, &tm_kvg, j * 128, y[0], y[1], y[2], y[3], cbar);
-          }
-          __syncwarp();
-          if (it + 1 < ntiles) next(it);  // the next tile's rows are looked up while the codes fly
-          const bool landed = __all_sync(kFull, mbar_wait(cbar, n_gather & 1u, p.status));
-          ++n_gather;
-          // the 8 codes of bf16 chunk (key kr, block j, piece pc), and their widened store
-          auto codes_at = [&](int kr, int j, int pc) -> uint2 {
-            const int c16 = ((j & 1) * 4 + (pc >> 1)) ^ (kr & 7);
-            return *reinterpret_cast<const uint2*>(stg + (j >> 1) * kBlkBytes + kr * 128 + c16 * 16 + (pc & 1) * 8);
-          };
-          auto put = [&](int kr, int j, int pc, uint2 c8) {
-            *reinterpret_cast<uint4*>(dst + j * kBlkBytes + kr * 128 + ((pc ^ (kr & 7)) << 4)) = e4m3x8_to_bf16x8(c8);
-          };
-          auto widen = [&](int j0, int j1) {  // blocks j0 .. j1 - 1
-#pragma unroll 4
-            for (int id = lt; id < kNk * (j1 - j0) * 8; id += kLoaders) {
-              const int kr = (id / 8) % kNk, j = j0 + id / (8 * kNk), pc = id % 8;
-              put(kr, j, pc, codes_at(kr, j, pc));
-            }
-          };
-          widen(0, 4);
-          if (named_sync_or(3, kLoaders, !landed)) {
-            *sAbort = 1;
-            break;
-          }
-          widen(4, 6);
-          named_sync(3, kLoaders);
-          widen(6, 7);
-          constexpr int kLastPer = (2 * kNk * 8 + kLoaders - 1) / kLoaders;  // 5
-          uint2 last[kLastPer];
-#pragma unroll
-          for (int k2 = 0; k2 < kLastPer; ++k2) {
-            const int id = lt + k2 * kLoaders;
-            last[k2] = id < 2 * kNk * 8 ? codes_at((id / 8) % kNk, 7 + id / (8 * kNk), id % 8) : make_uint2(0u, 0u);
-          }
-          named_sync(3, kLoaders);
-#pragma unroll
-          for (int k2 = 0; k2 < kLastPer; ++k2) {
-            const int id = lt + k2 * kLoaders;
-            if (id < 2 * kNk * 8) put((id / 8) % kNk, 7 + id / (8 * kNk), id % 8, last[k2]);
-          }
-          fence_proxy_async_smem();
-          named_sync(3, kLoaders);
+        } else if (fp8 && pool) {  // the wideners'
           if (lt == 0) mbar_arrive(&kfull[st]);
+          if (it + 1 < ntiles) next(it);
         } else {
           // consecutive threads take consecutive 16-byte chunks of a row (coalesced): chunk c of key
           // kr is 16-byte piece c & 7 of channel block c >> 3; FP8 entries are read as 8 codes and
-          // widened, in two passes to bound the registers they hold
+          // widened, in passes that bound the registers they hold
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint2 codes8[kHalfPer];
+          for (int half = 0; half < kPasses; ++half) {
+            uint2 codes8[kPer];
 #pragma unroll
-            for (int q = 0; q < kHalfPer; ++q) {
-              const int id = lt + (half * kHalfPer + q) * kLoaders;
+            for (int q = 0; q < kPer; ++q) {
+              const int id = lt + (half * kPer + q) * kLoaders;
               codes8[q] = make_uint2(0u, 0u);
-              if (id < kChunks) {
+              {
                 const int kr = id / (kNb * 8), c = id % (kNb * 8);
                 const uint32_t cd = sCode[kr];
                 if (fp8 && (cd >> kRowBits) == 1u) {
@@ -576,8 +542,8 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
             }
             if (fp8) {
 #pragma unroll
-              for (int q = 0; q < kHalfPer; ++q) {
-                const int id = lt + (half * kHalfPer + q) * kLoaders;
+              for (int q = 0; q < kPer; ++q) {
+                const int id = lt + (half * kPer + q) * kLoaders;
                 if (id < kChunks) {
                   const int kr = id / (kNb * 8), c = id % (kNb * 8);
                   if ((sCode[kr] >> kRowBits) == 1u)
@@ -595,29 +561,132 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
           if (lt == 0) mbar_arrive(&kfull[st]);
         }
       }
+    } else if (FP8 && tid >= kWidenThread0) {
+      // ------------------------------------------------------------ wideners
+      // A tile of FP8 pool rows: TMA gathers its E4M3 codes, four rows of 128 channels per copy (a missing row reads
+      // zeros), into five pieces of 64 swizzled 128-byte rows over the stage's last 40 KB; the rows are spread over
+      // the whole pool, and copies by the threads (cp.async) stood in line for their translations (4,400 cycles a
+      // tile). The codes are then widened to bf16 in place. Row kr of block 4 + i lies where row kr of piece i was,
+      // which holds blocks 2i and 2i + 1, and a warp has its eight keys' rows to itself: it goes through the blocks in
+      // order, two at a time, each pair read a step ahead, and no other warp has to wait for it. Lane l has the 16
+      // codes of key l % 8 in quarter l / 8 of every block: the swizzled pieces of a quarter warp's eight keys lie in
+      // different banks, in the loads and in the stores.
+      const int ww = warp - kWidenThread0 / 32, h = lane >> 3, kr = ww * 8 + (lane & 7);
+      const uint32_t from0 = kCodes0 + kr * 128 + ((h ^ (kr & 7)) << 4), from1 = from0 ^ 64u;  // even and odd blocks
+      const uint32_t to0 = kr * 128 + (((2 * h) ^ (kr & 7)) << 4), to1 = to0 ^ 16u;
+      for (int it = 0; it < ntiles; ++it) {
+        const uint32_t gt = g + it;
+        const int st = gt & 1;
+        bool okw = __shfl_sync(kFull, *sAbort, 0) == 0;
+        if (okw) okw = __all_sync(kFull, mbar_wait(&rdy[st], (gt >> 1) & 1u, p.status));
+        if (!okw) {
+          *sAbort = 1;
+          break;
+        }
+        uint8_t* dst = sK + st * kStageBytes;
+        const bool codes = __shfl_sync(kFull, sKind[st], 0) != 0;
+        if (codes) {
+          const uint32_t* sCode = sCodes + (Sm::kCodes == 1 ? 0 : st * kNk);
+          if (lane == 0) mbar_arrive_expect_tx(cbar, kPieces * 8 * 128);
+          __syncwarp();
+          if (lane < 2 * kPieces) {
+            const int j = lane >> 1, r4 = ww * 8 + (lane & 1) * 4;
+            int y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t cd = sCode[r4 + e];
+              y[e] = (cd >> kRowBits) == 1u ? static_cast<int>(cd & kRowMask) : -1;
+            }
+            tma_gather4(dst + kCodes0 + j * kBlkBytes + r4 * 128, &tm_kvg, j * 128, y[0], y[1], y[2], y[3], cbar);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(cfree);
+        if (codes) {
+          if (!__all_sync(kFull, mbar_wait(cbar, n_gather & 1u, p.status))) {
+            *sAbort = 1;
+            mbar_wait(cbar, n_gather & 1u, nullptr);  // once more: the copies may not outlive the block
+            break;
+          }
+          ++n_gather;
+          uint4 v = *reinterpret_cast<const uint4*>(dst + from0), w = *reinterpret_cast<const uint4*>(dst + from1);
+#pragma unroll 1
+          for (int s = 0; s < kPieces; ++s) {  // blocks 2s and 2s + 1 (the last pair has one block)
+            uint4 nv = make_uint4(0u, 0u, 0u, 0u), nw = nv;
+            if (s + 1 < kPieces) {
+              nv = *reinterpret_cast<const uint4*>(dst + from0 + (s + 1) * kBlkBytes);
+              if (2 * s + 3 < kNb) nw = *reinterpret_cast<const uint4*>(dst + from1 + (s + 1) * kBlkBytes);
+            }
+            const uint2 c[4] = {make_uint2(v.x, v.y), make_uint2(v.z, v.w), make_uint2(w.x, w.y), make_uint2(w.z, w.w)};
+            uint4 o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = widen8(c[i]);
+            if (nan_codes(c[0]) | nan_codes(c[1]) | nan_codes(c[2]) | nan_codes(c[3])) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[i] = set_nan(o[i], c[i]);
+            }
+            __syncwarp();  // blocks 4 to 8 overwrite codes that the warp has read by now
+            uint8_t* to = dst + 2 * s * kBlkBytes;
+            *reinterpret_cast<uint4*>(to + to0) = o[0];
+            *reinterpret_cast<uint4*>(to + to1) = o[1];
+            if (2 * s + 1 < kNb) {
+              *reinterpret_cast<uint4*>(to + kBlkBytes + to0) = o[2];
+              *reinterpret_cast<uint4*>(to + kBlkBytes + to1) = o[3];
+            }
+            v = nv;
+            w = nw;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&kfull[st]);
+      }
     } else if (warp == 4) {
-      // ------------------------------------------------------------ S issue (lane 0; the warp waits together)
+      // ------------------------------------------------------------ MMA issue
+      // One warp issues S of a tile and P V of the one before in the order in which they become possible. (P V from a
+      // softmax warp stood in the tensor cores' queue behind the next S: 2,200 cycles of every tile's softmax.)
       const uint32_t issuer = elect_one();
-      constexpr uint32_t idesc_s = umma_idesc_bf16(kH, kNk, false);
-      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kH, kNk, false), idesc_pv = umma_idesc_bf16(kH, 256, true);
+      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sPa = smem_u32(sP);
       bool ok = __all_sync(kFull, mbar_wait(qbar, n_item & 1u, p.status));
       tc_fence_after();
-      for (int it = 0; it < ntiles && ok; ++it) {
-        if (__shfl_sync(kFull, *sAbort, 0)) break;
-        const uint32_t gt = g + it;
-        const int k = __shfl_sync(kFull, gt & 1, 0);
-        // the stage is shared memory written by TMA or fenced cp.async / stores: the mbarrier
-        // orders it; S buffer k is free once the softmax has read S(gt - 2)
-        if (!(ok = __all_sync(kFull, mbar_wait(&kfull[k], (gt >> 1) & 1u, p.status)))) break;
-        if (gt >= 2 && !(ok = __all_sync(kFull, mbar_wait(&sfree[k], ((gt >> 1) - 1) & 1u, p.status)))) break;
-        tc_fence_after();
-        if (k == 0)  // the stage as a constant in each branch, so that the descriptors are
-          issue_s(issuer, tmem + kColS, sQa, sKa, idesc_s);
-        else
-          issue_s(issuer, tmem + kColS + kNk, sQa, sKa + kStageBytes, idesc_s);
-        commit_if(issuer, &sfull[k]);
-        __syncwarp();
+      int is = 0, ip = 0;  // tiles whose S, whose P V have been issued
+      uint32_t polls = 0;
+      while (ip < ntiles && ok) {
+        const uint32_t gp = __shfl_sync(kFull, g + ip, 0), gs = __shfl_sync(kFull, g + is, 0);
+        const int kp = gp & 1, k = gs & 1;
+        if (ip < is && mbar_done(pfull, gp & 1u)) {
+          tc_fence_after();
+          // channel blocks 0..7 of the tile: V
+          const uint64_t pd = umma_desc_sw128(sPa, 16, 1024), vd = umma_desc_sw128(sKa + kp * kStageBytes, kBlkBytes, 1024);
+#pragma unroll
+          for (int ks = 0; ks < kNk / 16; ++ks) {
+            const uint32_t acc = (ip > 0 || ks > 0) ? 1u : 0u;
+            umma_ss_if(issuer, tmem + kColO, pd + 2 * ks, vd + ks * 16 * 8, idesc_pv, acc);
+            umma_ss_if(issuer, tmem + kColO + kLane16, pd + 2 * ks, vd + 4 * kBlkBytes / 16 + ks * 16 * 8, idesc_pv, acc);
+          }
+          commit_if(issuer, &kempty[kp]);
+          commit_if(issuer, obar);
+          __syncwarp();
+          ++ip;
+          polls = 0;
+        } else if (is < ntiles && mbar_done(&kfull[k], (gs >> 1) & 1u) &&
+                   (gs < 2 || mbar_done(&sfree[k], ((gs >> 1) - 1) & 1u))) {
+          // the stage is shared memory written by TMA or fenced cp.async / stores: the mbarrier
+          // orders it; S buffer k is free once the softmax has read S(gs - 2)
+          tc_fence_after();
+          const uint32_t ks = __shfl_sync(kFull, k, 0);
+          issue_s(issuer, tmem + kColS + ks * kNk, sQa, sKa + ks * kStageBytes, idesc_s);
+          commit_if(issuer, &sfull[k]);
+          __syncwarp();
+          ++is;
+          polls = 0;
+        } else if ((++polls & 255u) == 0u) {  // bounded like every wait
+          ok = __shfl_sync(kFull, *sAbort, 0) == 0 && polls < kSpinLimit;
+          if (!ok && polls >= kSpinLimit) report(p.status, CSKV_ERR_TIMEOUT);
+        }
       }
+      commit_if(issuer, dbar);  // one completion per item, also after an abort
       if (!ok && lane == 0) *sAbort = 1;
       __syncwarp();
     } else if (warp < 4) {
@@ -626,15 +695,10 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
       const float sl2 = p.sm_scale * kLog2e;
       const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
       const int hr = warp * 16 + (lane & 15), kh = lane >> 4;
-      const uint32_t issuer = elect_one();
-      constexpr uint32_t idesc_pv = umma_idesc_bf16(kH, 256, true);
-      const uint32_t sKa = smem_u32(sK), sPa = smem_u32(sP);
       const float slope2 = RULE && p.slopes ? p.slopes[grp * kH + hr] * kLog2e : 0.f;
       uint8_t* prow = sP + hr * 128;
       float m_used = -INFINITY, l_run = 0.f;
       bool ok = true;
-      // Every softmax warp reaches the named barrier of every tile; a failed bounded wait only
-      // marks the tile bad, and the barrier's OR over the 128 threads decides for all of them.
       for (int it = 0; it < ntiles && ok; ++it) {
         const uint32_t gt = g + it;
         const int k = gt & 1;
@@ -664,10 +728,16 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
         uint32_t pp[16];
         if (good) {
           const uint32_t vm = sMask[k * 2 + kh];
-          const float* scl = sScale + k * kNk + 32 * kh;
+          const float4* scl = reinterpret_cast<const float4*>(sScale + k * kNk + 32 * kh);
           if (fp8) {  // an FP8 entry's logit and value carry its scale
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s[j] *= scl[j];
+            for (int j = 0; j < 32; j += 4) {
+              const float4 c = scl[j / 4];
+              s[j] *= c.x;
+              s[j + 1] *= c.y;
+              s[j + 2] *= c.z;
+              s[j + 3] *= c.w;
+            }
           }
           if constexpr (RULE) {
             const float4* pos = reinterpret_cast<const float4*>(sDist + k * kNk + 32 * kh);
@@ -705,11 +775,23 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
           const float msub = m_used == -INFINITY ? 0.f : m_used;
           float l0 = 0.f, l1 = 0.f;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float e0 = exp2f(s[2 * j] - msub), e1 = exp2f(s[2 * j + 1] - msub);
-            l0 += e0;
-            l1 += e1;
-            pp[j] = fp8 ? pack_bf16(e0 * scl[2 * j], e1 * scl[2 * j + 1]) : pack_bf16(e0, e1);
+          for (int j = 0; j < 16; j += 2) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e[i] = RULE ? ex2(s[2 * j + i] - msub) : exp2f(s[2 * j + i] - msub);
+            l0 += e[0];
+            l1 += e[1];
+            l0 += e[2];
+            l1 += e[3];
+            if (fp8) {
+              const float4 c = scl[j / 2];
+              e[0] *= c.x;
+              e[1] *= c.y;
+              e[2] *= c.z;
+              e[3] *= c.w;
+            }
+            pp[j] = pack_bf16(e[0], e[1]);
+            pp[j + 1] = pack_bf16(e[2], e[3]);
           }
           l_run += l0 + l1;
           // the P buffer was read by the P V of tile gt - 1, which also finished O
@@ -739,34 +821,13 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        // every row's P is in shared memory, or some warp met a wait that gave up (uniform answer)
-        if (named_sync_or(1, 128, !good || *sAbort)) {
+        if (!good || __shfl_sync(kFull, *sAbort, 0)) {
           *sAbort = 1;
           ok = false;
           break;
         }
-        if (warp == 0) {
-          tc_fence_after();
-          auto issue_pv = [&](uint32_t vb) {  // channel blocks 0..7 of the tile: V
-#pragma unroll
-            for (int ks = 0; ks < kNk / 16; ++ks) {
-              const uint64_t pa = umma_desc_sw128(sPa + ks * 32, 16, 1024);
-              const uint32_t acc = (it > 0 || ks > 0) ? 1u : 0u;
-              umma_ss_if(issuer, tmem + kColO, pa, umma_desc_sw128(vb + ks * 16 * 128, kBlkBytes, 1024), idesc_pv, acc);
-              umma_ss_if(issuer, tmem + kColO + kLane16, pa,
-                         umma_desc_sw128(vb + 4 * kBlkBytes + ks * 16 * 128, kBlkBytes, 1024), idesc_pv, acc);
-            }
-          };
-          if (__shfl_sync(kFull, k, 0) == 0)
-            issue_pv(sKa);
-          else
-            issue_pv(sKa + kStageBytes);
-          commit_if(issuer, &kempty[k]);
-          commit_if(issuer, obar);
-          __syncwarp();
-        }
+        mbar_arrive(pfull);
       }
-      if (warp == 0) commit_if(issuer, dbar);  // one completion per item, also after an abort
       // epilogue: normalised partial output of this split and head group, and its log-sum-exp
       ok = __all_sync(kFull, mbar_wait(dbar, n_item & 1u, p.status)) && ok;
       if (!ok) *sAbort = 1;
@@ -774,6 +835,9 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
       const float l_row = l_run + __shfl_xor_sync(kFull, l_run, 16);
       const int head = grp * kH + hr;
       const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+      // RULE: a query in one piece has its answer here, and the merge passes over it
+      const bool whole = RULE && p.rope_dims == 0 && sPref[b + 1] - sPref[b] == groups;
+      uint16_t* out = p.out + ((int64_t)b * p.n_heads + head) * kDv + kh * 256;
       // part_o is head-minor ([query x split][d_v / 4][heads][4]): the 16 lanes of a half-warp
       // write 16 consecutive heads, 256 contiguous bytes
       float4* po = reinterpret_cast<float4*>(p.part_o) +
@@ -785,6 +849,19 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
           tmem_ld32(tmem + lane_base + kColO + c, orow);
           tmem_ld_wait();
         }
+        if (whole) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 16) {
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = ok && l_row > 0.f ? pack_bf16(__uint_as_float(orow[q + 2 * i]) * inv, __uint_as_float(orow[q + 2 * i + 1]) * inv)
+                                       : 0u;
+            *reinterpret_cast<uint4*>(out + c + q) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(out + c + q + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+          continue;
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
           const float4 v = ok ? make_float4(__uint_as_float(orow[4 * q]) * inv, __uint_as_float(orow[4 * q + 1]) * inv,
@@ -793,9 +870,13 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
           po[(int64_t)(c / 4 + q) * p.n_heads] = v;
         }
       }
-      if (kh == 0)
-        p.part_lse[slot * p.n_heads + head] =
-            l_row > 0.f ? (m_used + log2f(l_row)) * kLn2 : -INFINITY;
+      if (kh == 0) {
+        const float lse = l_row > 0.f ? (m_used + log2f(l_row)) * kLn2 : -INFINITY;
+        if (!whole)
+          p.part_lse[slot * p.n_heads + head] = lse;
+        else if (p.lse)
+          p.lse[(int64_t)b * p.n_heads + head] = lse;
+      }
     }
     g += ntiles;
     tc_fence_before();

@@ -22,6 +22,16 @@ __device__ __forceinline__ bool named_sync_or(int id, int n, bool v) {
       : "memory");
   return r != 0;
 }
+// whether the phase of parity `parity` is complete, without waiting; every lane of the warp gets the same answer
+__device__ __forceinline__ bool mbar_done(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return __all_sync(kFull, ok != 0);
+}
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
