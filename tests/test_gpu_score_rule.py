@@ -379,3 +379,60 @@ def test_calls_repeat_bit_for_bit_and_replay(ck):
             torch.cuda.synchronize()
             assert torch.equal(out, a) and torch.equal(lse, la)
         del graph
+
+
+@pytest.mark.parametrize("H", [48, 80, 96, 128])
+def test_chunk_head_counts(ck, H):
+    """Head counts that do not divide the chunk form's tiles, and ones above its rows per query."""
+    n, pos0 = 403, 1700
+    pos = list(range(pos0, pos0 + n))
+    s = Setup(ck, "hca", 128, 128, H, [0] * n, pos, seed=H, chunk={0: (0, pos0, n)})
+    _both(s, rules=RULES[:2], queries=[0, 1, 2, 3, 5, 7, 100, 127, 128, 200, 401, 402])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_pair_form_keeps_a_bad_row_to_its_queries(ck, value):
+    """With inverse RoPE a chunk takes the query-pair form: the pair of a query that sees a bad token answers as before."""
+    n, pos0 = 640, 3000
+    s = Setup(ck, "hca", 128, 128, 64, [0] * n, list(range(pos0, pos0 + n)), seed=18, chunk={0: (0, pos0, n)})
+    token = pos0 + 301  # odd: the second query of its pair is the first to see it
+    s.x_chunk[token - pos0, 5] = value
+    out, _ = s.run(30.0, s.slopes, lse=False, rope_dims=32)
+    s.check(out, None, 30.0, s.slopes, [0, 1, 299, 300, 301 + N_WIN, 302 + N_WIN, n - 1], rope=32)
+
+
+def test_fp8_codes_of_every_value(ck):
+    """Entries of all finite E4M3 codes (subnormal ones and zeros of both signs included), and a NaN code that one query
+    has selected: the others answer as before."""
+    seqs, pos = [0, 1, 2, 0, 1, 2, 0], [3000, 2500, 1111, 2999, 700, 131, 40]
+    s = Setup(ck, "csa", 576, 512, 128, seqs, pos, k=200, fp8=True, seed=19)
+    codes = torch.randint(0, 254, s.L.kv_pool.shape, generator=s.g, device="cuda")
+    s.L.kv_pool.copy_((codes + (codes >= 127).int()).to(torch.uint8))  # 0x7f and 0xff are NaN
+    s.L.kv_scale.mul_(1 / 8)
+    _both(s, rules=RULES[:2])
+    row = s.L.rows_of(1, int(s.sel[1, 17]), 1)
+    s.L.kv_pool[row, 33] = 0x7F
+    out, lse = s.run(20.0, s.slopes)
+    hit = [i for i in range(len(pos)) if seqs[i] == 1 and int(s.sel[1, 17]) in s.sel[i, : int(s.cnt[i])].tolist()]
+    assert 1 in hit
+    s.check(out, lse, 20.0, s.slopes, [i for i in range(len(pos)) if i not in hit])
+
+
+@pytest.mark.parametrize("kind,fp8", [("csa", True), ("hca", True), ("csa", False)])
+def test_latent_576_chunk(ck, kind, fp8):
+    """A chunk's rows in the wide latent's window: tiles of several sources, FP8 entries among them."""
+    n, pos0 = 37, 1501
+    s = Setup(ck, kind, 576, 512, 64, [0] * n, list(range(pos0, pos0 + n)), k=100 if kind == "csa" else 0, fp8=fp8,
+              seed=20, chunk={0: (0, pos0, n)})
+    _both(s, rules=RULES[:2], queries=[0, 1, 17, 36])
+
+
+@pytest.mark.parametrize("d_qk,d_v,H,fp8", [(576, 512, 128, False), (576, 512, 64, True), (128, 128, 32, False)])
+def test_lengths_far_apart(ck, d_qk, d_v, H, fp8):
+    """One call's sequences from one token to 300,000: the keys are cut by the real lengths, and a query in one piece, or
+    with inverse RoPE through the merge, answers the same."""
+    pos = [5, 299999, 130, 90001, 0, 3000, 128 * 64, 40000]
+    s = Setup(ck, "hca", d_qk, d_v, H, list(range(8)), pos, fp8=fp8, seed=21)
+    _both(s, rules=RULES[:2])
+    out, lse = s.run(30.0, s.slopes, rope_dims=64)
+    s.check(out, lse, 30.0, s.slopes, rope=64)
