@@ -196,7 +196,8 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8]) {
 // The three forms of the kernel. kBounded: a cap of at most kMaxStatic (in log2 units) bounds every logit of a row to
 // [ref - cap2, ref + cap2] around a reference known beforehand, and the row's own token, or with a negative slope its
 // farthest key, reaches into that range, so 2^(s - ref) neither overflows fp32 nor vanishes, and the softmax needs no
-// running maximum: no pass for it, no agreement between the halves of a row, no rescaling (181 us -> STATIC us).
+// running maximum: no pass for it, no agreement between the halves of a row, no rescaling (181 us -> 176 us
+// when it came).
 enum Mode { kPlainMax, kCappedMax, kBounded };
 constexpr float kMaxStatic = 80.f;
 
@@ -880,12 +881,17 @@ bool encode_rows(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box
 
 // The plain form (no rule) keeps the kernels it has always run on, and so its results. Inverse RoPE stays with the
 // query-pair and split kernels: its fp64 sine and cosine do not fit the output warps' registers.
+//
+// Fewer than 32 rows per SM are better off with their keys split over the SMs, which this kernel does not do: it takes
+// 19 us for 2000 cached tokens, 29 us for 60,000 and 230 us for 1M whatever the rows up to 256 per SM, where the others
+// take 12, 17 and 67 us at 8 rows per SM (64 heads), 19, 30 and 237 us at 32, and 26, 49 and 466 us at 64. (With 16 heads
+// they fall behind at 16 rows per SM already: 19, 31 and 267 us.)
 bool attend_chunk_supported(const AttendParams& p, int n_sm) {
   const uint64_t pool_rows = static_cast<uint64_t>(p.n_pages) * p.page_size;
   const uint64_t ring_rows = static_cast<uint64_t>(p.n_seqs_layer) * p.n_win;
   const int64_t rows = (int64_t)p.n_q * p.n_heads;
   return !p.is_csa && has_score_rule(p) && p.x_chunk && p.rope_dims == 0 && p.d_qk == kD && p.d_v == kD && p.n_heads >= 16 &&
-         p.kv_dtype == CSKV_BF16 && rows >= (int64_t)kItemRows * n_sm / 2 && rows <= 0x7fffffff - (int64_t)kItemRows * (n_sm + 1) &&
+         p.kv_dtype == CSKV_BF16 && rows >= (int64_t)32 * n_sm && rows <= 0x7fffffff - (int64_t)kItemRows * (n_sm + 1) &&
          p.max_pos < (1 << 30) && p.n_win < (1 << 30) && p.chunk_len > 0 &&
          pool_rows <= kRowMask && ring_rows <= kRowMask && static_cast<uint64_t>(p.chunk_len) <= kRowMask;
 }
