@@ -16,7 +16,7 @@
 //   warps 0-15: softmax, two threads per row: warps 8 w + 4 h .. + 3 take keys
 //     64 h .. + 63 of tile w. (One thread per row, with two softmax warps on a
 //     scheduler, waited for its own instructions most of the time: 198 us where two
-//     take 181.) With a running maximum the two agree on the row's reference at a
+//     took 181.) With a running maximum the two agree on the row's reference at a
 //     barrier, and it moves only when a logit exceeds it by more than 2^8; O is
 //     rescaled then, half of its channels by each;
 //   warp 16: issues the MMAs;
