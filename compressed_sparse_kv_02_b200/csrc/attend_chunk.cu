@@ -172,7 +172,7 @@ struct Smem {
   static constexpr int BASE = SUM + 4 * kTileRows * 4;  // [2 tiles][128 rows] what a row's sum stands on
   static constexpr int ITEM = BASE + 2 * kTileRows * 4;  // [kItems] item descriptors
   static constexpr int BAR = ITEM + kItems * sizeof(ItemDesc);
-  static constexpr int TMEM = BAR + 32 * 8;
+  static constexpr int TMEM = BAR + 36 * 8;
   static constexpr int FLAGS = TMEM + 8;
   static constexpr int END = FLAGS + 8;
   static constexpr size_t bytes() { return 1024 + END; }
@@ -240,7 +240,7 @@ __device__ __forceinline__ void slow_row(const AttendParams& p, int64_t row, flo
 
 // Pipeline (key tiles numbered g over the CTA's items; stage g % 2):
 //   loader  : look up rows -> wait kempty (P V of tile g - 2) -> TMA gathers -> kfull
-//   MMA     : S0(0) S1(0), then per key tile: wait pfull0 -> P V 0(g), S0(g + 1) -> sfull0 (or odone0);
+//   MMA     : S0(0) S1(0), then per key tile (kBounded: per part of it): wait pfull0 -> P V 0(g), S0(g + 1) -> sfull0 (or odone0);
 //             wait pfull1 -> P V 1(g) -> kempty, S1(g + 1) -> sfull1 (or odone1); the last S1 of an item -> qempty
 //   softmax : wait sfull (S here, and every earlier P V of this tile done: O may be rescaled) -> P -> pfull;
 //             after the item's last tile: its rows' sums -> lready
@@ -253,6 +253,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_chunk16,
                         const __grid_constant__ AttendParams p, const __grid_constant__ Rule r) {
   constexpr bool CAP = MODE != kPlainMax;
+  // Parts of a key tile that go through S, softmax and P V one after another. Without a running maximum a part of 64 keys
+  // waits for nothing of the other: while the softmax is at one, P V and the next S of the other run, and its warps go
+  // from part to part (a whole tile's warps waited 2,400 of 6,500 cycles for it: 164.7 us, in parts 161.3; the rest is issue: 49% of the
+  // slots and 15 instructions a logit).
+  constexpr int kParts = MODE == kBounded ? 2 : 1, kPartKeys = kNk / kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = sm + Smem::Q;
@@ -265,9 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sBase = reinterpret_cast<float*>(sm + Smem::BASE);
   uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + Smem::BAR);  // [3] loaders (2) -> MMA, softmax
   uint64_t* kempty = kfull + kNS;                                 // [3] MMA -> loaders
-  uint64_t* sfull = kempty + kNS;                                 // [2] MMA -> softmax
-  uint64_t* pfull = sfull + 2;                                    // [2] softmax (8 warps) -> MMA
-  uint64_t* odone = pfull + 2;                                    // [2] MMA -> output warps
+  uint64_t* sfull = kempty + kNS;                                 // [2 tiles][kParts] MMA -> softmax
+  uint64_t* pfull = sfull + 4;                                    // [2 tiles][kParts] softmax (8 warps) -> MMA
+  uint64_t* odone = pfull + 4;                                    // [2] MMA -> output warps
   uint64_t* oread = odone + 2;                                    // [2] output warps (4) -> MMA
   uint64_t* qfull = oread + 2;                                    // [2] Q of the tile landed (TMA)
   uint64_t* qempty = qfull + 2;                                   // [2] the item's S products of the tile are done
@@ -289,9 +294,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ifull[i], 1);
       mbar_init(&ifree[i], 23);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pfull[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&odone[i], 1);
       mbar_init(&oread[i], 4);
       mbar_init(&lready[i], 8);
@@ -345,39 +352,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------------- MMA issue (lane 0; the warp waits together)
       const uint32_t issuer = elect_one();
-      constexpr uint32_t idesc_s = umma_idesc_bf16(kTileRows, kNk, false);
+      constexpr uint32_t idesc_s = umma_idesc_bf16(kTileRows, kPartKeys, false);
       constexpr uint32_t idesc_pv = umma_idesc_bf16(kTileRows, kD, true);
       const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK);
       auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(kFull, mbar_wait(bar, parity, p.status)); };
-      auto s_of = [&](int w, int st) {  // S of tile w from stage st: 8 K-steps over the two 64-channel halves
-        const uint32_t q = sQa + w * kStageBytes, k = sKa + st * kStageBytes;
+      auto s_of = [&](int w, int h, int st) {  // S of part h of tile w from stage st: 8 K-steps over the two channel halves
+        const uint32_t q = sQa + w * kStageBytes, k = sKa + st * kStageBytes + h * (kPartKeys * 128);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t off = (ks >> 2) * kHalfBytes + (ks & 3) * 32u;
-          umma_ss_if(issuer, tmem + kColS + w * kNk, umma_desc_sw128(q + off, 16, 1024), umma_desc_sw128(k + off, 16, 1024),
-                     idesc_s, ks > 0 ? 1u : 0u);
+          umma_ss_if(issuer, tmem + kColS + w * kNk + h * kPartKeys, umma_desc_sw128(q + off, 16, 1024),
+                     umma_desc_sw128(k + off, 16, 1024), idesc_s, ks > 0 ? 1u : 0u);
         }
       };
-      auto pv_of = [&](int w, int st, uint32_t acc) {  // O += P V of tile w: 8 K-steps of 16 keys
-        const uint32_t v = sKa + st * kStageBytes;
+      // O += P V of a part: K-steps of 16 keys. P of a thread's kPartKeys / 2 keys lies over the first half of their S.
+      auto pv_of = [&](int w, int h, int st, uint32_t acc) {
+        const uint32_t v = sKa + st * kStageBytes + h * (kPartKeys * 128);
+        constexpr int kSteps = kPartKeys / 16;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_ts_if(issuer, tmem + kColO + w * kD, tmem + kColS + w * kNk + (ks >> 2) * 64 + (ks & 3) * 8,
+        for (int ks = 0; ks < kSteps; ++ks)
+          umma_ts_if(issuer, tmem + kColO + w * kD,
+                     tmem + kColS + w * kNk + h * kPartKeys + (ks / (kSteps / 2)) * (kPartKeys / 2) + (ks % (kSteps / 2)) * 8,
                      umma_desc_sw128(v + ks * 16 * 128, kHalfBytes, 1024), idesc_pv, ks > 0 ? 1u : acc);
       };
       // the stage as a constant in each branch, so that the descriptors are
-      auto issue_s = [&](int w, uint32_t gt) {
+      auto issue_s = [&](int w, int h, uint32_t gt) {
         const uint32_t st = gt % kNS;
-        if (st == 0) s_of(w, 0);
-        else if (st == 1) s_of(w, 1);
-        else s_of(w, 2);
-        commit_if(issuer, &sfull[w]);
+        if (st == 0) s_of(w, h, 0);
+        else if (st == 1) s_of(w, h, 1);
+        else s_of(w, h, 2);
+        commit_if(issuer, &sfull[w * kParts + h]);
       };
-      auto issue_pv = [&](int w, uint32_t gt, bool acc) {
+      auto issue_pv = [&](int w, int h, uint32_t gt, bool acc) {
         const uint32_t st = gt % kNS;
-        if (st == 0) pv_of(w, 0, acc);
-        else if (st == 1) pv_of(w, 1, acc);
-        else pv_of(w, 2, acc);
+        if (st == 0) pv_of(w, h, 0, acc);
+        else if (st == 1) pv_of(w, h, 1, acc);
+        else pv_of(w, h, 2, acc);
       };
       static_assert(kNS == 3, "the stage branches");
       // the items with keys, found one ahead: S of the next item's first key tile is issued behind P V of this
@@ -399,12 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int ntot = next_tiles();
       if (ntot && ok) {
-        for (int w = 0; w < 2 && ok; ++w) {
-          ok = wait(&qfull[w], 0) && wait(&kfull[0], 0);
+#pragma unroll
+        for (int i = 0; i < 2 * kParts; ++i) {
+          const int h = i >> 1, w = i & 1;
+          ok = ok && wait(&qfull[w], 0) && wait(&kfull[0], 0);
           if (!ok) break;
           tc_fence_after();
-          issue_s(w, 0);
-          if (ntot == 1) commit_if(issuer, &qempty[w]);
+          issue_s(w, h, 0);
+          if (ntot == 1 && h == kParts - 1) commit_if(issuer, &qempty[w]);
         }
       }
       while (ntot && ok) {
@@ -419,19 +431,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool last = it + 1 == ntot, more = !last || nnext > 0;
           const bool qlast = last ? nnext == 1 : it + 2 == ntot;  // the next S is the last one of its item
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            ok = wait(&pfull[w], gt & 1u) && (it > 0 || n_act == 0 || wait(&oread[w], (n_act - 1) & 1u));
+          for (int i = 0; i < 2 * kParts; ++i) {
+            const int h = i >> 1, w = i & 1;
+            ok = wait(&pfull[w * kParts + h], gt & 1u) &&
+                 (h > 0 || it > 0 || n_act == 0 || wait(&oread[w], (n_act - 1) & 1u));
             if (!ok) break;
             tc_fence_after();
-            issue_pv(w, gt, it > 0);
-            if (w == 1) commit_if(issuer, &kempty[gt % kNS]);
-            if (last) commit_if(issuer, &odone[w]);
+            issue_pv(w, h, gt, h > 0 || it > 0);
+            if (i == 2 * kParts - 1) commit_if(issuer, &kempty[gt % kNS]);
+            if (last && h == kParts - 1) commit_if(issuer, &odone[w]);
             if (more) {
               ok = (!last || wait(&qfull[w], (n_act + 1) & 1u)) && wait(&kfull[gn % kNS], (gn / kNS) & 1u);
               if (!ok) break;
               tc_fence_after();
-              issue_s(w, gn);
-              if (qlast) commit_if(issuer, &qempty[w]);
+              issue_s(w, h, gn);
+              if (qlast && h == kParts - 1) commit_if(issuer, &qempty[w]);
             }
             __syncwarp();
           }
@@ -674,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp >> 3, hf = (warp >> 2) & 1, tr = (warp & 3) * 32 + lane;  // tile, key half, row of the tile
     const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     // S of my keys (their P goes over its first 32 columns)
-    const uint32_t sb = trow + kColS + w * kNk + 64 * hf;
+    const uint32_t sb = trow + kColS + w * kNk + 64 * hf;  // (kBounded: by parts)
     const uint32_t ob = trow + kColO + w * kD + 64 * hf;  // O of my channels (rescaling)
     float* side = sSide + (2 * w + hf) * kTileRows + tr;
     float* other = sSide + (2 * w + (hf ^ 1)) * kTileRows + tr;
@@ -720,24 +734,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int st = gt % kNS;
           // the stage's positions and key bits were written before kfull; that phase cannot move on before this
           // thread's P has been used
-          bool good = __all_sync(kFull, mbar_wait(&sfull[w], gt & 1u, p.status)) &&
+          bool good = __all_sync(kFull, mbar_wait(&sfull[w * kParts], gt & 1u, p.status)) &&
                       __all_sync(kFull, mbar_wait(&kfull[st], (gt / kNS) & 1u, p.status));
           tc_fence_after();
           if constexpr (MODE == kBounded) {
-            if (!good) {
-              fail = true;
-              break;
-            }
-            uint32_t sa[32], sc[32];
-            tmem_ld32(sb, sa);
-            tmem_ld_wait();
-            tmem_ld32(sb + 32, sc);
             const float nr = -slope2 * static_cast<float>(shift) - ref;
-            const float4* pos4 = reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf);
-            auto part = [&](int c, uint32_t (&s)[32]) {
-              apply_rule<true>(s, pos4 + 8 * c, r, slope2, nr);
-              const int a = k * kNk + 64 * hf + 32 * c;
-              const uint32_t vm = sMask[st * 4 + 2 * hf + c] & (range_bits(a, lo, hi) | range_bits(a, n_w, end));
+#pragma unroll 1
+            for (int h = 0; h < kParts; ++h) {
+              if (h > 0) good = __all_sync(kFull, mbar_wait(&sfull[w * kParts + h], gt & 1u, p.status));
+              if (!good) {
+                fail = true;
+                break;
+              }
+              tc_fence_after();
+              const int at = 64 * h + 32 * hf;  // this thread's keys of the part
+              uint32_t s[32];
+              tmem_ld32(trow + kColS + w * kNk + at, s);
+              tmem_ld_wait();
+              apply_rule<true>(s, reinterpret_cast<const float4*>(sPos + st * kNk + at), r, slope2, nr);
+              const int a = k * kNk + at;
+              const uint32_t vm = sMask[st * 4 + 2 * h + hf] & (range_bits(a, lo, hi) | range_bits(a, n_w, end));
               if (__any_sync(kFull, vm != kFull)) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -751,15 +767,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else l_a = __fadd2_rn(l_a, e);
                 pp[j] = pack_bf16(e.x, e.y);
               }
-              tmem_st16(sb + 16 * c, pp);
-            };
-            part(0, sa);
-            tmem_ld_wait();
-            part(1, sc);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[w]);
+              tmem_st16(trow + kColS + w * kNk + at, pp);
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&pfull[w * kParts + h]);
+            }
+            if (fail) break;
             continue;
           }
           uint32_t s[64];
