@@ -38,11 +38,12 @@
 //     the softmax warps are at the next item (as a part of their work it took a
 //     third of an item's time).
 // A row's segment is the run of consecutive queries of one sequence it stands in
-// (positions at most kMaxStep apart, so that a segment's windows overlap): the key
+// (positions at most kMaxStep apart, so that a segment's windows overlap), and an
+// item is the 256 rows with one of their segments: the key
 // list of a segment is its queries' window positions wlo .. thi, padded to a
 // multiple of four, then the entries visible at thi, and each row's mask keeps its
-// own window and entries. Rows that
-// belong to another segment of the item are masked out of the whole segment.
+// own window and entries. Rows of
+// another segment are masked out.
 //
 // Masked keys are multiplied by P = 0, which a NaN or an infinity in a masked key's
 // row would turn into NaN. A row whose output is not finite is therefore taken again
@@ -104,8 +105,10 @@ __device__ __forceinline__ int visible32(const AttendParams& p, int t, int lm) {
 __device__ __forceinline__ int start32(const AttendParams& p, int t) { return max(t - p.n_win + 1, 0); }
 
 // An item as one warp describes it to the others: its queries (at most 17: 16 heads or more, rows that need
-// not begin with a query) and its segments. The other roles keep a few numbers of it in registers at a time, which
-// leaves a softmax thread room for its 64 logits.
+// not begin with a query) and one segment of them. The rows of its other segments are other items: on their way through
+// the grid the 256 rows come up once per segment they may have (pass), on another CTA each time, so that 16 single tokens
+// with long contexts of their own, which share no key, are 16 CTAs' work (64 such tokens at 1M beside a chunk of 1024, 16
+// heads: 250 us, one CTA for all segments of 256 rows 3,211, the other kernels 341).
 struct Segment {
   int s, e;         // queries s .. e - 1 of the item
   int n_w, ntiles;  // window places of the key list, key tiles
@@ -115,17 +118,25 @@ struct Segment {
 struct ItemDesc {
   int row0;  // first row (-1: no more items)
   int h0;    // its head
-  int nseg, ntot;
+  int nseg, ntot;  // 1 and its key tiles, or 0 and 0: rows without keys only
+  int pass;
+  int pad[3];
   int t[20];  // each query's position, -1 without keys
-  Segment seg[17];
+  Segment seg;
 };
 constexpr int kItems = 4;  // descriptors in flight
 static_assert(sizeof(ItemDesc) % 16 == 0 && sizeof(Segment) == 32, "descriptor layout");
 
-// Describes the item whose first row is `row0` = head h0 of query q0, one query per lane.
-__device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int row0, int q0, int h0, int rows, int lm,
-                                         int lane) {
-  int t = -1, seq = -1;
+// as many passes over the items as 256 rows have queries at most
+__host__ __device__ __forceinline__ int item_passes(int n_heads) {
+  return kItemRows % n_heads == 0 ? kItemRows / n_heads : (kItemRows - 2 + n_heads) / n_heads + 1;
+}
+
+// The queries of the 256 rows from `row0` = head h0 of query q0 on, one per lane: its position (-1: without keys) and
+// sequence; returns the lanes where a segment begins.
+__device__ __forceinline__ unsigned find_segments(const AttendParams& p, int row0, int q0, int h0, int rows, int lane, int& t,
+                                                  int& seq) {
+  t = seq = -1;
   if (lane * p.n_heads < min(kItemRows, rows - row0) + h0) {
     const int64_t pos = p.q_pos[q0 + lane];
     seq = p.q_seq[q0 + lane];
@@ -134,10 +145,18 @@ __device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int
   const int tp = __shfl_up_sync(kFull, t, 1);
   const int sp = __shfl_up_sync(kFull, seq, 1);
   const bool cont = lane > 0 && tp >= 0 && sp == seq && abs(t - tp) <= kMaxStep;
-  const unsigned starts = __ballot_sync(kFull, t >= 0 && !cont), runs = __ballot_sync(kFull, t >= 0);
+  return __ballot_sync(kFull, t >= 0 && !cont);
+}
+
+// Describes segment `pass` of them.
+__device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int row0, int h0, unsigned starts, int pass, int t,
+                                         int seq, int lm, int lane) {
+  const unsigned runs = __ballot_sync(kFull, t >= 0);
   if (lane < 20) d.t[lane] = t;
-  int ntot = 0, i = 0;
-  for (unsigned m = starts; m; m &= m - 1, ++i) {
+  int ntot = 0;
+  if (starts) {
+    unsigned m = starts;
+    for (int i = 0; i < pass; ++i) m &= m - 1;
     Segment g;
     g.s = __ffs(m) - 1;
     const unsigned stop = (starts | ~runs) & ~((2u << g.s) - 1u);  // the first lane past s that begins another or none
@@ -149,15 +168,15 @@ __device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int
     g.wlo = start32(p, __reduce_min_sync(kFull, mine));
     g.n_w = (g.thi - g.wlo + 4) & ~3;
     g.n = g.n_w + visible32(p, g.thi, lm);
-    g.ntiles = (g.n + kNk - 1) / kNk;
-    ntot += g.ntiles;
-    if (lane == 0) d.seg[i] = g;
+    ntot = g.ntiles = (g.n + kNk - 1) / kNk;
+    if (lane == 0) d.seg = g;
   }
   if (lane == 0) {
     d.row0 = row0;
     d.h0 = h0;
-    d.nseg = i;
+    d.nseg = starts ? 1 : 0;
     d.ntot = ntot;
+    d.pass = pass;
   }
 }
 
@@ -487,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++q_issued;
         uint32_t gt = g;
-        for (int i = 0; i < d.nseg && ok; ++i) {
-          const Segment sg = d.seg[i];
+        {
+          const Segment sg = d.seg;
           for (int it = 0; it < sg.ntiles; ++it, ++gt) {
             const int st = gt % kNS;
             // keys u .. u + 3 of the list: all window places, or all entries (of one page)
@@ -588,43 +607,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     else if (warp == kItemWarp) {
       // ---------------------------------------------------------------- items
-      int row0 = blockIdx.x * kItemRows, q0 = row0 / p.n_heads, h0 = row0 % p.n_heads;
-      const int step = gridDim.x * kItemRows, dq = step / p.n_heads, dh = step % p.n_heads;
+      // each pass begins at another CTA
+      const int passes = item_passes(p.n_heads);
+      const int shift = max(static_cast<int>(gridDim.x) / passes, 1), n_items = (rows + kItemRows - 1) / kItemRows;
       bool ok = true;
-      for (; ok; ++n_item) {
+      auto slot = [&]() {  // the next descriptor, once everyone has given it back
         ok = __all_sync(kFull, n_item < kItems || mbar_wait(&ifree[n_item % kItems], ((n_item / kItems) - 1) & 1u, p.status));
-        if (!ok) break;
-        ItemDesc& d = items[n_item % kItems];
-        if (row0 < rows)
-          describe(p, d, row0, q0, h0, rows, lm, lane);
-        else if (lane == 0)
-          d.row0 = -1;
+        return ok;
+      };
+      auto publish = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ifull[n_item % kItems]);
-        if (row0 >= rows) break;
-        row0 += step;
-        q0 += dq;
-        h0 += dh;
-        if (h0 >= p.n_heads) {
-          h0 -= p.n_heads;
-          ++q0;
+        ++n_item;
+      };
+      for (int pass = 0; pass < passes && ok; ++pass) {
+        for (int idx = (blockIdx.x + pass * shift) % gridDim.x; idx < n_items; idx += gridDim.x) {
+          const int row0 = idx * kItemRows, q0 = row0 / p.n_heads, h0 = row0 % p.n_heads;
+          int t, seq;
+          const unsigned starts = find_segments(p, row0, q0, h0, rows, lane, t, seq);
+          if (pass > 0 && __popc(starts) <= pass) continue;
+          if (!slot()) break;
+          describe(p, items[n_item % kItems], row0, h0, starts, pass, t, seq, lm, lane);
+          publish();
         }
+      }
+      if (ok && slot()) {
+        if (lane == 0) items[n_item % kItems].row0 = -1;
+        publish();
       }
       if (!ok) *sAbort = 1;
     } else {
       // ---------------------------------------------------------------- outputs: O / l in bf16, and the log-sum-exp
       const int tr = (warp & 3) * 32 + lane;  // row of the tile
       const uint32_t otile = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO;
+      const float inv_heads = 1.f / static_cast<float>(p.n_heads);
       bool ok = true;
       for (; ok; ++n_item) {
         if (!(ok = item_wait(n_item))) break;
         const ItemDesc& d = items[n_item % kItems];
         if (d.row0 < 0) break;
         const int ntot = d.ntot;
+        // this item's rows: its segment's, and in the first pass those without keys
+        uint32_t own = 0;
+        const int lo = d.nseg ? d.seg.s : 0, hi = d.nseg ? d.seg.e : 0;
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          const int qi = static_cast<int>((static_cast<float>(d.h0 + w * kTileRows + tr) + 0.5f) * inv_heads);
+          if (d.row0 + w * kTileRows + tr < rows && ((qi >= lo && qi < hi) || (d.pass == 0 && d.t[qi] < 0))) own |= 1u << w;
+        }
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           const int row = d.row0 + w * kTileRows + tr;
-          const bool in = row < rows;
+          const bool in = (own >> w) & 1u;
           ok = __all_sync(kFull, mbar_wait(&lready[w], n_item & 1u, p.status));
           if (!ok) break;
           const float l = sSum[2 * w * kTileRows + tr] + sSum[(2 * w + 1) * kTileRows + tr];
@@ -718,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = 0.f;
       if (MODE == kBounded && slope2 < 0.f && t >= 0)
         ref = -slope2 * (visible32(p, t, lm) > 0 ? entry_distance(t, 0, p.m) : static_cast<float>(t - start32(p, t)));
-      for (int i = 0; i < d.nseg && ok && !fail; ++i) {
-        const Segment& sg = d.seg[i];
+      if (d.nseg) {
+        const Segment& sg = d.seg;
         // this row's keys in the segment's list: window lo .. hi - 1, entries n_w .. end - 1
         const int n_w = sg.n_w, ntiles = sg.ntiles;
         int lo = 0, hi = 0, end = 0;
@@ -926,7 +960,7 @@ cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
               : p.score_cap * kLog2e <= kMaxStatic ? attend_chunk_kernel<kBounded> : attend_chunk_kernel<kCappedMax>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int64_t items = (rows + kItemRows - 1) / kItemRows;
+  const int64_t items = (rows + kItemRows - 1) / kItemRows * item_passes(p.n_heads);
   return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q,
                     tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, p, make_rule(p.sm_scale, p.score_cap));
 }

@@ -436,3 +436,22 @@ def test_lengths_far_apart(ck, d_qk, d_v, H, fp8):
     _both(s, rules=RULES[:2])
     out, lse = s.run(30.0, s.slopes, rope_dims=64)
     s.check(out, lse, 30.0, s.slopes, rope=64)
+
+
+@pytest.mark.parametrize("H", [16, 48, 64])
+def test_single_tokens_beside_a_chunk(ck, H):
+    """Decode tokens of many sequences in one call with a chunk: next to each other, they share no key."""
+    chunk, seqs, pos = {0: (0, 900, 330)}, [0] * 330, list(range(900, 1230))
+    for s in range(1, 41):
+        seqs.append(s)
+        pos.append((s * 977) % 6000)
+        if s % 3:  # its token in the chunk's rows; the others' in the ring
+            chunk[s] = (329 + s, pos[-1], 1)
+    order = list(range(0, 330, 2)) + list(range(330, 370)) + list(range(1, 330, 2))  # the chunk's tokens on both sides
+    s = Setup(ck, "hca", 128, 128, H, [seqs[i] for i in order], [pos[i] for i in order], seed=H + 22, chunk=chunk)
+    s.q_pos[180] = -1  # one of the single tokens is invalid: zeros, and its neighbours as ever
+    for cap, bias in RULES[:3]:
+        slopes = s.slopes if bias else None
+        out, lse = s.run(cap, slopes, want=ck.ERR_INVALID_ARG)
+        assert not bool(out[180].any()) and bool((lse[180] == -math.inf).all())
+        s.check(out, lse, cap, slopes, [0, 1, 77, 164] + [i for i in range(165, 205) if i != 180] + [205, 206, 300, 369])
