@@ -19,12 +19,16 @@ template <typename F>
 __device__ __forceinline__ int plan_split(const AttendParams& p, int unit, int slots, int lane, F keys_of) {
   const int most = p.keys_per_split / unit;
   if (p.n_q >= slots) return most * unit;
+  auto tiles_of = [&](int b) { return static_cast<int>((keys_of(b) + unit - 1) / unit); };
+  constexpr int kHeld = 3;  // the first 96 queries' tiles stay in registers: counting them takes loads and wide divisions
+  int held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) held[i] = lane + 32 * i < p.n_q ? tiles_of(lane + 32 * i) : 0;
   auto pieces = [&](int per) {
     int n = 0;
-    for (int b = lane; b < p.n_q; b += 32) {
-      const int tiles = static_cast<int>((keys_of(b) + unit - 1) / unit);
-      n += (tiles + per - 1) / per;
-    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) n += (held[i] + per - 1) / per;
+    for (int b = lane + 32 * kHeld; b < p.n_q; b += 32) n += (tiles_of(b) + per - 1) / per;
     return static_cast<int>(__reduce_add_sync(kFull, n));
   };
   int lo = (pieces(1) + slots - 1) / slots, hi = most;
