@@ -128,6 +128,9 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
   const int mt = warp % MT, vs = warp / MT;
   const int g = lane >> 2, c = lane & 3;
   const int n_groups = p.n_heads / HG;
+  // The launch overlaps the tail of the kernel ahead of this one. (The merge is not let in early: its blocks would take
+  // their places beside the last ones here, 17.2 us instead of 16.0 for 32 queries of 640 keys.)
+  grid_dependency_wait();
   const int kps = RULE ? plan_split(p, KT, p.slots, lane, [&](int b) { return query_keys(p, b).n; }) : p.keys_per_split;
 
   // items per query: splits * head groups; exclusive prefix in shared memory
@@ -380,6 +383,7 @@ __device__ __forceinline__ int pieces_of(const AttendParams& p, int b, int64_t& 
 // d_v / 4 threads per head, four channels each; the split loop issues eight
 // independent loads at a time.
 __global__ void __launch_bounds__(256) attend_merge_kernel(AttendParams p) {
+  grid_dependency_wait();  // the partial outputs come from the attention kernel ahead of this one
   const int b = blockIdx.x;
   int64_t first;
   const int ns = pieces_of(p, b, first);
@@ -527,8 +531,7 @@ cudaError_t run_attend_form(AttendParams& p, int n_sm, cudaStream_t st) {
   if (grid < 1) grid = 1;
   const int64_t want = (int64_t)n_sm * per_sm / groups, most = (int64_t)p.n_q * p.max_splits;
   p.slots = static_cast<int>(want < most ? want : most);
-  kern<<<static_cast<int>(grid), 32 * MT * VS, smem, st>>>(p);
-  e = cudaGetLastError();
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(32 * MT * VS), smem, st, p);
   if (e != cudaSuccess) return e;
   return launch_attend_merge(p, st);
 }
@@ -563,8 +566,7 @@ cudaError_t launch_attend_merge(AttendParams& p, cudaStream_t st) {
   }
   const int hb = 256 / (p.d_v / 4);
   dim3 mg(static_cast<unsigned>(p.n_q), static_cast<unsigned>((p.n_heads + hb - 1) / hb));
-  attend_merge_kernel<<<mg, 256, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_pdl(attend_merge_kernel, mg, dim3(256), 0, st, p);
 }
 
 bool attend_supported(int d_qk, int d_v, int n_heads, int kv_dtype) {
