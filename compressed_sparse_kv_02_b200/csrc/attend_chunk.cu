@@ -119,9 +119,9 @@ struct ItemDesc {
   int row0;  // first row (-1: no more items)
   int h0;    // its head
   int nseg, ntot;  // 1 and its key tiles, or 0 and 0: rows without keys only
-  int pass;
-  int pad[3];
-  int t[20];  // each query's position, -1 without keys
+  int pad[4];
+  uint8_t own[32];  // a bit per row: the item writes it (its segment's rows, and in the first pass those without keys)
+  int t[20];        // each query's position, -1 without keys
   Segment seg;
 };
 constexpr int kItems = 4;  // descriptors in flight
@@ -149,11 +149,11 @@ __device__ __forceinline__ unsigned find_segments(const AttendParams& p, int row
 }
 
 // Describes segment `pass` of them.
-__device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int row0, int h0, unsigned starts, int pass, int t,
-                                         int seq, int lm, int lane) {
+__device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int row0, int h0, int rows, unsigned starts, int pass,
+                                         int t, int seq, int lm, int lane) {
   const unsigned runs = __ballot_sync(kFull, t >= 0);
   if (lane < 20) d.t[lane] = t;
-  int ntot = 0;
+  int ntot = 0, lo = 0, hi = 0;
   if (starts) {
     unsigned m = starts;
     for (int i = 0; i < pass; ++i) m &= m - 1;
@@ -170,13 +170,20 @@ __device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int
     g.n = g.n_w + visible32(p, g.thi, lm);
     ntot = g.ntiles = (g.n + kNk - 1) / kNk;
     if (lane == 0) d.seg = g;
+    lo = g.s;
+    hi = g.e;
   }
+  uint32_t own = 0;  // of rows 8 lane .. + 7
+  for (int i = 0, at = h0 + 8 * lane; i < 8; ++i, ++at) {
+    const int qi = at / p.n_heads, tq = __shfl_sync(kFull, t, qi);
+    own |= (row0 + 8 * lane + i < rows && ((qi >= lo && qi < hi) || (pass == 0 && tq < 0)) ? 1u : 0u) << i;
+  }
+  d.own[lane] = static_cast<uint8_t>(own);
   if (lane == 0) {
     d.row0 = row0;
     d.h0 = h0;
     d.nseg = starts ? 1 : 0;
     d.ntot = ntot;
-    d.pass = pass;
   }
 }
 
@@ -607,8 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     else if (warp == kItemWarp) {
       // ---------------------------------------------------------------- items
-      // each pass begins at another CTA
-      const int passes = item_passes(p.n_heads);
+      // Several sequences: each pass begins at another CTA. One sequence: its queries mostly follow each other, and the
+      // CTA of the rows takes all their segments (the look at every item in each pass took 9 of 177 us).
+      const int passes = p.chunk_desc ? item_passes(p.n_heads) : 1;
       const int shift = max(static_cast<int>(gridDim.x) / passes, 1), n_items = (rows + kItemRows - 1) / kItemRows;
       bool ok = true;
       auto slot = [&]() {  // the next descriptor, once everyone has given it back
@@ -625,10 +633,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row0 = idx * kItemRows, q0 = row0 / p.n_heads, h0 = row0 % p.n_heads;
           int t, seq;
           const unsigned starts = find_segments(p, row0, q0, h0, rows, lane, t, seq);
-          if (pass > 0 && __popc(starts) <= pass) continue;
-          if (!slot()) break;
-          describe(p, items[n_item % kItems], row0, h0, starts, pass, t, seq, lm, lane);
-          publish();
+          const int n_seg = __popc(starts), stop = passes > 1 ? min(pass + 1, max(n_seg, 1)) : max(n_seg, 1);
+          for (int i = pass; i < stop && slot(); ++i) {  // rows without any segment are an item of the first pass
+            describe(p, items[n_item % kItems], row0, h0, rows, starts, i, t, seq, lm, lane);
+            publish();
+          }
+          if (!ok) break;
         }
       }
       if (ok && slot()) {
@@ -640,25 +650,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- outputs: O / l in bf16, and the log-sum-exp
       const int tr = (warp & 3) * 32 + lane;  // row of the tile
       const uint32_t otile = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO;
-      const float inv_heads = 1.f / static_cast<float>(p.n_heads);
       bool ok = true;
       for (; ok; ++n_item) {
         if (!(ok = item_wait(n_item))) break;
         const ItemDesc& d = items[n_item % kItems];
         if (d.row0 < 0) break;
         const int ntot = d.ntot;
-        // this item's rows: its segment's, and in the first pass those without keys
-        uint32_t own = 0;
-        const int lo = d.nseg ? d.seg.s : 0, hi = d.nseg ? d.seg.e : 0;
-#pragma unroll 1
-        for (int w = 0; w < 2; ++w) {
-          const int qi = static_cast<int>((static_cast<float>(d.h0 + w * kTileRows + tr) + 0.5f) * inv_heads);
-          if (d.row0 + w * kTileRows + tr < rows && ((qi >= lo && qi < hi) || (d.pass == 0 && d.t[qi] < 0))) own |= 1u << w;
-        }
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           const int row = d.row0 + w * kTileRows + tr;
-          const bool in = (own >> w) & 1u;
+          const bool in = (d.own[(w * kTileRows + tr) >> 3] >> (tr & 7)) & 1u;
           ok = __all_sync(kFull, mbar_wait(&lready[w], n_item & 1u, p.status));
           if (!ok) break;
           const float l = sSum[2 * w * kTileRows + tr] + sSum[(2 * w + 1) * kTileRows + tr];
@@ -960,7 +961,7 @@ cudaError_t launch_attend_chunk(AttendParams& p, int n_sm, cudaStream_t st) {
               : p.score_cap * kLog2e <= kMaxStatic ? attend_chunk_kernel<kBounded> : attend_chunk_kernel<kCappedMax>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int64_t items = (rows + kItemRows - 1) / kItemRows * item_passes(p.n_heads);
+  const int64_t items = (rows + kItemRows - 1) / kItemRows * (p.chunk_desc ? item_passes(p.n_heads) : 1);
   return launch_pdl(kern, dim3(static_cast<unsigned>(items < n_sm ? items : n_sm)), dim3(kThreads), smem, st, tm_q,
                     tm_pool, tm_ring, tm_chunk, tm_pool16, tm_ring16, tm_chunk16, p, make_rule(p.sm_scale, p.score_cap));
 }
