@@ -1,0 +1,56 @@
+"""GPU tests of csa_attend / hca_attend at the edges of what the header allows: buffers at any 16-byte boundary.
+
+Where a result is compared with the 64-bit formula, the bound is that of test_gpu_score_rule.
+"""
+import pytest
+import torch
+
+from test_gpu_score_rule import Setup
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ck(cskv_built):
+    import compressed_sparse_kv_02_b200 as ck
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return ck
+
+
+def _at_16(t):
+    """The same values at an address that is 16 bytes past a 32-byte boundary."""
+    n = 16 // t.element_size()
+    buf = torch.empty(t.numel() + n, dtype=t.dtype, device=t.device)
+    assert buf.data_ptr() % 32 == 0
+    view = buf[n:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+# the split kernel, the latent kernel (bf16, FP8), the query-pair kernel (selection; inverse RoPE) and the chunk form
+FORMS = [("hca", 128, 128, 32, 3, False, 0), ("csa", 128, 128, 16, 5, True, 0), ("hca", 576, 512, 64, 3, False, 0),
+         ("csa", 576, 512, 128, 5, True, 0), ("csa", 128, 128, 64, 640, False, 0), ("hca", 128, 128, 64, 640, False, 32),
+         ("hca", 128, 128, 64, 700, False, 0), ("hca", 128, 128, 16, 700, False, 0)]
+
+
+@pytest.mark.parametrize("kind,d_qk,d_v,H,n_q,fp8,rope", FORMS)
+@pytest.mark.parametrize("cap,bias", [(30.0, True), (70.0, False), (0.0, True), (0.0, False)])
+def test_buffers_need_16_byte_alignment_only(ck, kind, d_qk, d_v, H, n_q, fp8, rope, cap, bias):
+    """Outputs and inputs at addresses 16 bytes past a 32-byte boundary: the same bits."""
+    pos = list(range(1500, 1500 + n_q))
+    s = Setup(ck, kind, d_qk, d_v, H, [0] * n_q, pos, k=64 if kind == "csa" else 0, fp8=fp8, seed=H + n_q,
+              chunk={0: (0, 1500, n_q)})
+    slopes = s.slopes if bias else None
+    good, good_lse = s.run(cap, slopes, rope_dims=rope)
+    s.q, s.x_chunk = _at_16(s.q), _at_16(s.x_chunk)
+    s.L.ring_x, s.L.kv_pool = _at_16(s.L.ring_x), _at_16(s.L.kv_pool)
+    out, lse = _at_16(torch.full_like(good, 7.0)), torch.full_like(good_lse, 7.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(x_chunk=s.x_chunk, chunk_pos0=1500, status=st, score_cap=cap, slopes=slopes, rope_dims=rope)
+    if s.k:
+        ck.csa_attend(s.L, s.q_seq, s.q_pos, max(pos), s.q, s.sel, s.cnt, out, lse, **kw)
+    else:
+        ck.hca_attend(s.L, s.q_seq, s.q_pos, max(pos), s.q, out, lse, **kw)
+    assert ck.cskv_get_status(st) == ck.OK
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
