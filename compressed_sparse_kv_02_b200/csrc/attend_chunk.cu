@@ -120,8 +120,8 @@ struct Segment {
 struct ItemDesc {
   int row0;  // first row (-1: no more items)
   int h0;    // its head
-  int nseg, ntot;  // 1 and its key tiles, or 0 and 0: rows without keys only
-  int pad[4];
+  int ntot;  // key tiles (0 with the end)
+  int pad[5];
   uint8_t own[32];  // a bit per row: the item writes it (its segment's rows, and in the first pass those without keys)
   int t[20];        // each query's position, -1 without keys
   Segment seg;
@@ -150,42 +150,46 @@ __device__ __forceinline__ unsigned find_segments(const AttendParams& p, int row
   return __ballot_sync(kFull, t >= 0 && !cont);
 }
 
+// Rows of which none has a key, by one warp: zeros and -inf. They are no item: the MMA warp looks for the next item's
+// descriptor before it has finished its own, so every published one has key tiles to work on.
+__device__ __forceinline__ void write_empty(const AttendParams& p, int row0, int rows, int lane) {
+  const int n = min(kItemRows, rows - row0);
+  uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)row0 * kD);
+  for (int i = lane; i < n * (kD / 8); i += 32) out[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (p.lse)
+    for (int i = lane; i < n; i += 32) p.lse[(int64_t)row0 + i] = -INFINITY;
+}
+
 // Describes segment `pass` of them.
 __device__ __forceinline__ void describe(const AttendParams& p, ItemDesc& d, int row0, int h0, int rows, unsigned starts, int pass,
                                          int t, int seq, int lm, int lane) {
   const unsigned runs = __ballot_sync(kFull, t >= 0);
   if (lane < 20) d.t[lane] = t;
-  int ntot = 0, lo = 0, hi = 0;
-  if (starts) {
-    unsigned m = starts;
-    for (int i = 0; i < pass; ++i) m &= m - 1;
-    Segment g;
-    g.s = __ffs(m) - 1;
-    const unsigned stop = (starts | ~runs) & ~((2u << g.s) - 1u);  // the first lane past s that begins another or none
-    g.e = stop ? __ffs(stop) - 1 : 32;
-    g.seq = __shfl_sync(kFull, seq, g.s);
-    const int ts = __shfl_sync(kFull, t, g.s);
-    const int mine = lane >= g.s && lane < g.e ? t : ts;
-    g.thi = __reduce_max_sync(kFull, mine);
-    g.wlo = start32(p, __reduce_min_sync(kFull, mine));
-    g.n_w = (g.thi - g.wlo + 4) & ~3;
-    g.n = g.n_w + visible32(p, g.thi, lm);
-    ntot = g.ntiles = (g.n + kNk - 1) / kNk;
-    if (lane == 0) d.seg = g;
-    lo = g.s;
-    hi = g.e;
-  }
+  unsigned m = starts;
+  for (int i = 0; i < pass; ++i) m &= m - 1;
+  Segment g;
+  g.s = __ffs(m) - 1;
+  const unsigned stop = (starts | ~runs) & ~((2u << g.s) - 1u);  // the first lane past s that begins another or none
+  g.e = stop ? __ffs(stop) - 1 : 32;
+  g.seq = __shfl_sync(kFull, seq, g.s);
+  const int ts = __shfl_sync(kFull, t, g.s);
+  const int mine = lane >= g.s && lane < g.e ? t : ts;
+  g.thi = __reduce_max_sync(kFull, mine);
+  g.wlo = start32(p, __reduce_min_sync(kFull, mine));
+  g.n_w = (g.thi - g.wlo + 4) & ~3;
+  g.n = g.n_w + visible32(p, g.thi, lm);
+  g.ntiles = (g.n + kNk - 1) / kNk;
   uint32_t own = 0;  // of rows 8 lane .. + 7
   for (int i = 0, at = h0 + 8 * lane; i < 8; ++i, ++at) {
     const int qi = at / p.n_heads, tq = __shfl_sync(kFull, t, qi);
-    own |= (row0 + 8 * lane + i < rows && ((qi >= lo && qi < hi) || (pass == 0 && tq < 0)) ? 1u : 0u) << i;
+    own |= (row0 + 8 * lane + i < rows && ((qi >= g.s && qi < g.e) || (pass == 0 && tq < 0)) ? 1u : 0u) << i;
   }
   d.own[lane] = static_cast<uint8_t>(own);
   if (lane == 0) {
     d.row0 = row0;
     d.h0 = h0;
-    d.nseg = starts ? 1 : 0;
-    d.ntot = ntot;
+    d.ntot = g.ntiles;
+    d.seg = g;
   }
 }
 
@@ -380,7 +384,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&ifree[n % kItems]);
   };
   uint32_t g = 0;      // key tiles before the current item
-  uint32_t n_act = 0;  // items with keys before the current one
 
   if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n");
@@ -425,22 +428,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         else pv_of(w, h, 2, acc);
       };
       static_assert(kNS == 3, "the stage branches");
-      // the items with keys, found one ahead: S of the next item's first key tile is issued behind P V of this
-      // item's last one, so the softmax of a tile goes from item to item without a pause
+      // The items, found one ahead: S of the next item's first key tile is issued behind P V of this item's last one, so
+      // the softmax of a tile goes from item to item without a pause. (The wait for the next descriptor does not depend
+      // on this item: its slot came free with the item kItems before it.)
       bool ok = true;
-      auto next_tiles = [&]() {  // key tiles of the next item that has any, 0 at the end
-        while (ok) {
-          if (!(ok = item_wait(n_item))) break;
-          const ItemDesc& d = items[n_item % kItems];
-          const int row0 = __shfl_sync(kFull, d.row0, 0), n = __shfl_sync(kFull, d.ntot, 0);
-          item_done(n_item++);
-          if (row0 < 0) {
-            --n_item;  // the end stays where it is
-            return 0;
-          }
-          if (n) return n;
-        }
-        return 0;
+      uint32_t n_act = 0;  // items done (n_item: items found)
+      auto next_tiles = [&]() {  // key tiles of the next item, 0 at the end (one exit: another spills)
+        ok = item_wait(n_item);
+        const int n = __shfl_sync(kFull, items[n_item % kItems].ntot, 0);
+        item_done(n_item++);
+        return ok ? n : 0;
       };
       int ntot = next_tiles();
       if (ntot && ok) {
@@ -507,11 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ItemDesc& d = items[n_item % kItems];
         const int row0 = d.row0, ntot = d.ntot;
         if (row0 < 0) break;
-        if (ntot == 0) {
-          item_done(n_item);
-          continue;
-        }
-        ok = __all_sync(kFull, n_act == 0 || mbar_wait(&qempty[half], (n_act - 1) & 1u, p.status));
+        ok = __all_sync(kFull, n_item == 0 || mbar_wait(&qempty[half], (n_item - 1) & 1u, p.status));
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&qfull[half], kStageBytes);
@@ -612,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         item_done(n_item);
         g += ntot;
-        ++n_act;
       }
       if (!ok) {  // the copies in flight get a bounded chance to land before the block leaves
         *sAbort = 1;
@@ -642,8 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int row0 = idx * kItemRows, q0 = row0 / p.n_heads, h0 = row0 % p.n_heads;
           int t, seq;
           const unsigned starts = find_segments(p, row0, q0, h0, rows, lane, t, seq);
-          const int n_seg = __popc(starts), stop = passes > 1 ? min(pass + 1, max(n_seg, 1)) : max(n_seg, 1);
-          for (int i = pass; i < stop && slot(); ++i) {  // rows without any segment are an item of the first pass
+          if (starts == 0 && pass == 0) write_empty(p, row0, rows, lane);
+          const int n_seg = __popc(starts), stop = passes > 1 ? min(pass + 1, n_seg) : n_seg;
+          for (int i = pass; i < stop && slot(); ++i) {
             describe(p, items[n_item % kItems], row0, h0, rows, starts, i, t, seq, lm, lane);
             publish();
           }
@@ -651,7 +644,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (ok && slot()) {
-        if (lane == 0) items[n_item % kItems].row0 = -1;
+        if (lane == 0) {
+          items[n_item % kItems].row0 = -1;
+          items[n_item % kItems].ntot = 0;
+        }
         publish();
       }
       if (!ok) *sAbort = 1;
@@ -665,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = item_wait(n_item))) break;
         const ItemDesc& d = items[n_item % kItems];
         if (d.row0 < 0) break;
-        const int ntot = d.ntot;
 #pragma unroll 1
         for (int w = 0; w < 2; ++w) {
           const int row = d.row0 + w * kTileRows + tr;
@@ -676,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float base = sBase[w * kTileRows + tr];
           __syncwarp();
           if (lane == 0) mbar_arrive(&lfree[w]);
-          if (ntot > 0 && !(ok = __all_sync(kFull, mbar_wait(&odone[w], n_act & 1u, p.status)))) break;
+          if (!(ok = __all_sync(kFull, mbar_wait(&odone[w], n_item & 1u, p.status)))) break;
           tc_fence_after();
           const bool has = in && l > 0.f;
           const float inv = has ? 1.f / l : 0.f;
@@ -684,10 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < kD; c += 16) {
             uint32_t o[16], v[8];
-            if (ntot > 0) {
-              tmem_ld16(otile + w * kD + c, o);
-              tmem_ld_wait();
-            }
+            tmem_ld16(otile + w * kD + c, o);
+            tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               o[e] = has ? __float_as_uint(__uint_as_float(o[e]) * inv) : 0u;
@@ -700,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the next item's first P V overwrites O: this warp's reads of it are complete
           tc_fence_before();
           __syncwarp();
-          if (ntot > 0 && lane == 0) mbar_arrive(&oread[w]);
+          if (lane == 0) mbar_arrive(&oread[w]);
           float lse = has ? (base + log2f(l)) * kLn2 : -INFINITY;
           const unsigned redo = __ballot_sync(kFull, in && (l != l || !(odd == 0.f)));
           if (redo) __syncwarp();
@@ -721,7 +714,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         item_done(n_item);
-        if (ntot > 0) ++n_act;
       }
       if (!ok) *sAbort = 1;
     }
@@ -763,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = 0.f;
       if (MODE == kBounded && slope2 < 0.f && t >= 0)
         ref = -slope2 * (visible32(p, t, lm) > 0 ? entry_distance(t, 0, p.m) : static_cast<float>(t - start32(p, t)));
-      if (d.nseg) {
+      {
         const Segment& sg = d.seg;
         // this row's keys in the segment's list: window lo .. hi - 1, entries n_w .. end - 1
         const int n_w = sg.n_w, ntiles = sg.ntiles;

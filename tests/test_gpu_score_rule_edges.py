@@ -54,3 +54,45 @@ def test_buffers_need_16_byte_alignment_only(ck, kind, d_qk, d_v, H, n_q, fp8, r
         ck.hca_attend(s.L, s.q_seq, s.q_pos, max(pos), s.q, out, lse, **kw)
     assert ck.cskv_get_status(st) == ck.OK
     assert torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
+# which queries of 4096 (64 heads: four queries share 256 rows; 16 heads: sixteen) have no keys
+EMPTY = {
+    "tail": lambda i, n: i >= n * 9 // 16,           # a padded batch
+    "head": lambda i, n: i < n * 7 // 16,
+    "blocks": lambda i, n: (i // 600) % 2 == 1,      # runs far longer than a block's rows
+    "one left": lambda i, n: i != n // 2,
+    "scattered": lambda i, n: (i * 2654435761 >> 7) % 19 < 18,
+    "all": lambda i, n: True,
+}
+
+
+@pytest.mark.parametrize("empty", list(EMPTY))
+@pytest.mark.parametrize("H,several", [(64, False), (16, False), (64, True), (16, True)])
+@pytest.mark.parametrize("cap,bias", [(30.0, True), (70.0, True), (0.0, True)])
+def test_chunk_with_many_queries_without_keys(ck, empty, H, several, cap, bias):
+    """Whole blocks of invalid positions in a chunk (padding): zeros and -inf for them, the others' answers, no other
+    report. Some blocks of rows then have no key at all, several in a row for one CTA."""
+    n, pos0 = 4096, 700
+    seqs, pos, chunk = [0] * n, list(range(pos0, pos0 + n)), {0: (0, pos0, n)}
+    if several:  # two sequences, described by chunk_desc
+        seqs = [0] * (n // 2) + [1] * (n - n // 2)
+        pos = list(range(pos0, pos0 + n // 2)) * 2
+        chunk = {0: (0, pos0, n // 2), 1: (n // 2, pos0, n // 2)}
+    s = Setup(ck, "hca", 128, 128, H, seqs, pos, seed=H, chunk=chunk)
+    gone = torch.tensor([EMPTY[empty](i, n) for i in range(n)], device="cuda")
+    s.q_pos = torch.where(gone, -1, s.q_pos)
+    out, lse = s.run(cap, s.slopes, want=ck.ERR_INVALID_ARG)
+    assert not bool(out[gone].any()) and bool((lse[gone] == -float("inf")).all())
+    live = (~gone).nonzero().flatten().tolist()
+    s.check(out, lse, cap, s.slopes, sorted(set(live[:3] + live[-3:] + live[:: max(1, len(live) // 12)])))
+
+
+def test_chunk_of_queries_of_unknown_sequences(ck):
+    """The same with sequence ids outside the layer, and without lse."""
+    n, pos0 = 2000, 300
+    s = Setup(ck, "hca", 128, 128, 64, [0] * n, list(range(pos0, pos0 + n)), seed=3, chunk={0: (0, pos0, n)})
+    s.q_seq[40:1960] = 7
+    out, _ = s.run(20.0, s.slopes, want=ck.ERR_OUT_OF_RANGE, lse=False)
+    assert not bool(out[40:1960].any())
+    s.check(out, None, 20.0, s.slopes, [0, 39, 1960, 1999])
