@@ -51,6 +51,8 @@
 // row would turn into NaN. A row whose output is not finite is therefore taken again
 // by its warp from its own keys only (slow_row), so that no key outside a query's
 // own set can reach its answer.
+#include <float.h>
+
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
@@ -233,12 +235,13 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], b
 }
 
 // The three forms of the kernel. kBounded: a cap of at most kMaxStatic (in log2 units) bounds every logit of a row to
-// [ref - cap2, ref + cap2] around a reference known beforehand, and the row's own token, or with a negative slope its
-// farthest key, reaches into that range, so 2^(s - ref) neither overflows fp32 nor vanishes, and the softmax needs no
+// ref + cap2 at most, for a reference known beforehand, and the row's own token, or with a negative slope its
+// farthest key, is at ref - cap2 at least, so 2^(s - ref) neither overflows fp32 nor vanishes, and the softmax needs no
 // running maximum: no pass for it, no agreement between the halves of a row, no rescaling (181 us -> 176 us
-// when it came).
+// when it came). Where that farthest key's page is missing the others may vanish: a sum below kMinSum, which the key
+// alone would exceed, has its row taken again (slow_row). Above it a term that 2^-126 flushes to zero is at most 2^-36 of it.
 enum Mode { kPlainMax, kCappedMax, kBounded };
-constexpr float kMaxStatic = 80.f;
+constexpr float kMaxStatic = 80.f, kMinSum = 0x1p-90f;
 
 // One row from its own keys only, by one warp (lane = 4 channels): scores in fp32, an online softmax, fp32 P.
 template <bool CAP>
@@ -695,7 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&oread[w]);
           float lse = has ? (base + log2f(l)) * kLn2 : -INFINITY;
-          const unsigned redo = __ballot_sync(kFull, in && (l != l || !(odd == 0.f)));
+          bool again = in && (!(l <= FLT_MAX) || !(odd == 0.f));
+          if (MODE == kBounded && in && l < kMinSum) again = d.t[(d.h0 + w * kTileRows + tr) / p.n_heads] >= 0;
+          const unsigned redo = __ballot_sync(kFull, again);
           if (redo) __syncwarp();
           for (unsigned left = redo; left; left &= left - 1) {
             const int b = __ffs(left) - 1;  // one row at a time, by the whole warp, over what its thread stored
@@ -751,10 +756,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;
       bool fail = false;  // kBounded: a wait gave up (the item's barrier tells the others)
       float2 l_a = make_float2(0.f, 0.f), l_b = l_a;
-      // kBounded: the reference, 0 where near keys lead and the farthest key's bias where far ones do
+      // kBounded: the reference, 0 where near keys lead and the farthest key's bias where far ones do. (Entry 0 stands at
+      // the middle of its block, so while the window begins before that its first token is the farther one.)
       float ref = 0.f;
-      if (MODE == kBounded && slope2 < 0.f && t >= 0)
-        ref = -slope2 * (visible32(p, t, lm) > 0 ? entry_distance(t, 0, p.m) : static_cast<float>(t - start32(p, t)));
+      if (MODE == kBounded && slope2 < 0.f && t >= 0) {
+        const float first = static_cast<float>(t - start32(p, t));
+        ref = -slope2 * (visible32(p, t, lm) > 0 ? fmaxf(entry_distance(t, 0, p.m), first) : first);
+      }
       {
         const Segment& sg = d.seg;
         // this row's keys in the segment's list: window lo .. hi - 1, entries n_w .. end - 1

@@ -5,7 +5,7 @@ Where a result is compared with the 64-bit formula, the bound is that of test_gp
 import pytest
 import torch
 
-from test_gpu_score_rule import Setup
+from test_gpu_score_rule import N_WIN, Setup
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,54 @@ def test_chunk_of_queries_of_unknown_sequences(ck):
     out, _ = s.run(20.0, s.slopes, want=ck.ERR_OUT_OF_RANGE, lse=False)
     assert not bool(out[40:1960].any())
     s.check(out, None, 20.0, s.slopes, [0, 39, 1960, 1999])
+
+
+def _small(s, std):
+    """Keys of the given standard deviation (Setup's have 2): values that leave a sum's overflow alone."""
+    for t in (s.L.kv_pool, s.L.ring_x, s.x_chunk):
+        t.mul_(std / 2)
+
+
+@pytest.mark.parametrize("cap", [20.0, 50.0, 55.0])
+@pytest.mark.parametrize("lo,hi", [(-1.0, -5.0), (-1.3, -1.7), (-2.4, -2.6), (-2.9, -3.1), (-0.01, -1.0)])
+def test_steep_negative_slopes_near_the_first_entry(ck, cap, lo, hi):
+    """Far keys lead, and at positions 128 to 190 the window's first token is farther than the middle of entry 0."""
+    H, pos = 64, list(range(100, 321))
+    for seed in range(4):
+        s = Setup(ck, "hca", 128, 128, H, [0] * len(pos), pos, seed=seed, chunk={0: (0, 100, len(pos))}, q_std=1.0)
+        _small(s, 128 ** -0.5)
+        slopes = torch.linspace(lo, hi, H, device="cuda")
+        out, lse = s.run(cap, slopes)
+        s.check(out, lse, cap, slopes)
+
+
+def _mask_entries(s, lo, hi):
+    """The 64-bit formula's keys without entries lo .. hi - 1 (whose page is missing)."""
+    rows = s.rows
+
+    def kept(i):
+        r, p = rows(i)
+        j = (p - (s.m - 1) / 2) / s.m
+        n_w = min(s.positions[i] + 1, N_WIN)
+        keep = torch.ones(p.numel(), dtype=torch.bool, device="cuda")
+        keep[n_w:] = (j[n_w:] < lo) | (j[n_w:] >= hi)
+        return r[keep], p[keep]
+
+    s.rows = kept
+
+
+@pytest.mark.parametrize("cap", [20.0, 55.0, 70.0, 0.0])
+@pytest.mark.parametrize("H,n_q", [(64, 300), (32, 5)])
+def test_a_missing_first_page_under_a_negative_slope(ck, cap, H, n_q):
+    """The key that leads has no row (reported): the others' answer, as with any missing page."""
+    pos0 = 128 * 40
+    s = Setup(ck, "hca", 128, 128, H, [0] * n_q, list(range(pos0, pos0 + n_q)), seed=5, chunk={0: (0, pos0, n_q)},
+              page_size=16, q_std=1.0)
+    _small(s, 128 ** -0.5)
+    slopes = -torch.exp2(torch.linspace(-9, 1, H, device="cuda"))
+    _mask_entries(s, 0, 16)
+    page = int(s.L.page_table[0, 0])
+    s.L.page_table[0, 0] = -1
+    out, lse = s.run(cap, slopes, want=ck.ERR_OUT_OF_RANGE)
+    s.L.page_table[0, 0] = page
+    s.check(out, lse, cap, slopes, range(0, n_q, max(1, n_q // 20)))
