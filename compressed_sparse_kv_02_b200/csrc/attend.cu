@@ -91,6 +91,12 @@ __device__ __forceinline__ uintptr_t key_row(const AttendParams& p, int b, int s
   return reinterpret_cast<uintptr_t>(static_cast<const uint16_t*>(p.kv_pool) + row * p.d_qk);
 }
 
+// The distance of query b's farthest key (it has keys): a row with a negative slope takes its distances relative to it.
+// The partial log-sum-exps are relative too; the query's first piece leaves that key's bias in lse, and the merge adds it.
+__device__ __forceinline__ float farthest(const AttendParams& p, int b, const QueryKeys& qk) {
+  const int64_t j = qk.n_c == 0 ? -1 : p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k]) : 0;
+  return far_distance(qk.t, qk.ws, j, p.m, p.n_win);
+}
 template <int DQK, int MT>
 struct AttnSmem {
   static constexpr int SROW = DQK + 8;  // padded row: ldmatrix rows fall in distinct banks
@@ -218,10 +224,14 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
     uint32_t qa[HOIST_Q ? DQK / 16 : 1][4];
     const bool cap = RULE && p.score_cap > 0.f;
     const float sl2 = cap ? p.sm_scale / p.score_cap : p.sm_scale * kLog2e;
-    float slope2[2] = {0.f, 0.f};
-    if (RULE && p.slopes) {
-      slope2[0] = p.slopes[grp * HG + mt * 16 + g] * kLog2e;
-      slope2[1] = p.slopes[grp * HG + mt * 16 + g + 8] * kLog2e;
+    float slope2[2] = {0.f, 0.f}, far[2] = {0.f, 0.f};  // far: what a row's distances are relative to
+    if (RULE && p.slopes) {  // (no branch on a slope: its load is waited for at the first softmax)
+      const float fd = farthest(p, b, qk);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        slope2[i] = p.slopes[grp * HG + mt * 16 + g + 8 * i] * kLog2e;
+        far[i] = slope2[i] < 0.f ? fd : 0.f;
+      }
     }
 
     for (int it = 0; it < ntiles; ++it) {
@@ -289,9 +299,9 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
             if (!RULE)
               v = sacc[nt][e] * sl2 * sc;
             else if (cap)
-              v = ruled_score<true>(sacc[nt][e] * sc, sl2, p.score_cap * kLog2e, slope2[e >> 1], sDist[i]);
+              v = ruled_score<true>(sacc[nt][e] * sc, sl2, p.score_cap * kLog2e, slope2[e >> 1], sDist[i] - far[e >> 1]);
             else
-              v = ruled_score<false>(sacc[nt][e] * sc, sl2, 0.f, slope2[e >> 1], sDist[i]);
+              v = ruled_score<false>(sacc[nt][e] * sc, sl2, 0.f, slope2[e >> 1], sDist[i] - far[e >> 1]);
           }
           pr[nt][e] = v;
           mx[e >> 1] = fmaxf(mx[e >> 1], v);
@@ -364,6 +374,11 @@ __global__ void __launch_bounds__(32 * MT * VS) attend_kernel(AttendParams p) {
     if (vs == 0 && c == 0) {
       p.part_lse[prow0] = l_run[0] > 0.f ? (m_run[0] + log2f(l_run[0])) * kLn2 : -INFINITY;
       p.part_lse[prow1] = l_run[1] > 0.f ? (m_run[1] + log2f(l_run[1])) * kLn2 : -INFINITY;
+      if (RULE && p.slopes && p.lse && split == 0) {
+        float* lse = p.lse + (int64_t)b * p.n_heads + head0;
+        lse[0] = -slope2[0] * far[0] * kLn2;
+        lse[8] = -slope2[1] * far[1] * kLn2;
+      }
     }
     __syncthreads();  // shared memory is reused by the next item
   }
@@ -392,6 +407,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(AttendParams p) {
   const int c4 = (threadIdx.x % (p.d_v / 4)) * 4;
   for (int h = blockIdx.y * hb + hl; h < p.n_heads && hl < hb; h += gridDim.y * hb) {
     const int64_t base = first * p.n_heads + h;
+    const float far = p.slopes && p.lse && c4 == 0 && ns > 0 ? p.lse[(int64_t)b * p.n_heads + h] : 0.f;
     float L = -INFINITY;
     for (int s = 0; s < ns; ++s) L = fmaxf(L, p.part_lse[base + (int64_t)s * p.n_heads]);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -425,7 +441,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(AttendParams p) {
     inverse_rope4(v, c4, p.d_v, p.rope_dims, p.rope_base, p.q_pos[b]);
     uint2 packed = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
     *reinterpret_cast<uint2*>(p.out + ((int64_t)b * p.n_heads + h) * p.d_v + c4) = packed;
-    if (p.lse && c4 == 0) p.lse[(int64_t)b * p.n_heads + h] = wsum > 0.f ? L + logf(wsum) : -INFINITY;
+    if (p.lse && c4 == 0) p.lse[(int64_t)b * p.n_heads + h] = wsum > 0.f ? L + logf(wsum) + far : -INFINITY;
   }
 }
 
@@ -445,6 +461,7 @@ __global__ void __launch_bounds__(256) attend_merge_t_kernel(AttendParams p) {
   const int g4 = blockIdx.y * 2 + (threadIdx.x >> 7);  // group of 4 output channels
   if (h >= p.n_heads || g4 >= p.d_v / 4) return;
   const int64_t lbase = first * p.n_heads + h;
+  const float far = p.slopes && p.lse && g4 == 0 && ns > 0 ? p.lse[(int64_t)b * p.n_heads + h] : 0.f;
   const float4* po = reinterpret_cast<const float4*>(p.part_o);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float wsum = 0.f;
@@ -507,7 +524,7 @@ __global__ void __launch_bounds__(256) attend_merge_t_kernel(AttendParams p) {
   inverse_rope4(v, g4 * 4, p.d_v, p.rope_dims, p.rope_base, p.q_pos[b]);
   const uint2 packed = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   *reinterpret_cast<uint2*>(p.out + ((int64_t)b * p.n_heads + h) * p.d_v + g4 * 4) = packed;
-  if (p.lse && g4 == 0) p.lse[(int64_t)b * p.n_heads + h] = wsum > 0.f ? L + logf(wsum) : -INFINITY;
+  if (p.lse && g4 == 0) p.lse[(int64_t)b * p.n_heads + h] = wsum > 0.f ? L + logf(wsum) + far : -INFINITY;
 }
 
 struct Plan {

@@ -246,11 +246,12 @@ constexpr float kMaxStatic = 80.f, kMinSum = 0x1p-90f;
 // One row from its own keys only, by one warp (lane = 4 channels): scores in fp32, an online softmax, fp32 P.
 template <bool CAP>
 __device__ __forceinline__ void slow_row(const AttendParams& p, int64_t row, float sl2, float cap2, float slope2, float (&o)[4],
-                                      float& m, float& l, int lane) {
+                                      float& m, float& l, float& far, int lane) {
   const int b = static_cast<int>(row / p.n_heads);
   const int t = static_cast<int>(p.q_pos[b]), ws = start32(p, t);
   const int seq = p.q_seq[b];
   const int n_w = t - ws + 1, n = n_w + visible32(p, t, __ffs(p.m) - 1);
+  far = slope2 < 0.f ? far_distance(t, ws, 0, p.m, p.n_win) : 0.f;  // m is relative to its bias
   const uint2 qv = *reinterpret_cast<const uint2*>(p.q + row * kD + 4 * lane);
   const __nv_bfloat162* q2 = reinterpret_cast<const __nv_bfloat162*>(&qv);
   const float2 qa = __bfloat1622float2(q2[0]), qb = __bfloat1622float2(q2[1]);
@@ -268,7 +269,7 @@ __device__ __forceinline__ void slow_row(const AttendParams& p, int64_t row, flo
 #pragma unroll
     for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(kFull, s, w);
     const float dist = u < n_w ? static_cast<float>(t - ws - u) : entry_distance(t, u - n_w, p.m);
-    s = ruled_score<CAP>(s, sl2, cap2, slope2, dist);
+    s = ruled_score<CAP>(s, sl2, cap2, slope2, dist - far);
     const float mn = fmaxf(m, s), corr = m == -INFINITY ? 0.f : exp2f(m - mn);
     const float e = s == -INFINITY ? 0.f : exp2f(s - mn);
     l = l * corr + e;
@@ -706,14 +707,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int b = __ffs(left) - 1;  // one row at a time, by the whole warp, over what its thread stored
             const int rr = __shfl_sync(kFull, row, b);
             const float slope2 = p.slopes ? p.slopes[rr % p.n_heads] * kLog2e : 0.f;
-            float o4[4], m, lr;
-            slow_row<CAP>(p, rr, r.pre.x, r.cap2.x, slope2, o4, m, lr, lane);
+            float o4[4], m, lr, far;
+            slow_row<CAP>(p, rr, r.pre.x, r.cap2.x, slope2, o4, m, lr, far, lane);
             const float iv = 1.f / lr;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o4[e] *= iv;
             *reinterpret_cast<uint2*>(p.out + (int64_t)rr * kD + 4 * lane) =
                 make_uint2(pack_bf16(o4[0], o4[1]), pack_bf16(o4[2], o4[3]));
-            if (lane == b) lse = (m + log2f(lr)) * kLn2;
+            if (lane == b) lse = (m + log2f(lr)) * kLn2 - slope2 * far * kLn2;
           }
           if (in && p.lse) p.lse[row] = lse;
         }
@@ -751,18 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qi = static_cast<int>((static_cast<float>(at) + 0.5f) * inv_heads);
       const float slope2 = p.slopes && in ? p.slopes[at - qi * p.n_heads] * kLog2e : 0.f;
       const int t = in ? d.t[qi] : -1;
-      float m_used = -INFINITY, l_run = 0.f;
+      float l_run = 0.f;
+      bool fresh = true;  // before the row's first key
       int shift = 0;  // the row's logits are taken at distance 0 of its segment's last query
       int it = 0;
       bool fail = false;  // kBounded: a wait gave up (the item's barrier tells the others)
       float2 l_a = make_float2(0.f, 0.f), l_b = l_a;
-      // kBounded: the reference, 0 where near keys lead and the farthest key's bias where far ones do. (Entry 0 stands at
-      // the middle of its block, so while the window begins before that its first token is the farther one.)
-      float ref = 0.f;
-      if (MODE == kBounded && slope2 < 0.f && t >= 0) {
-        const float first = static_cast<float>(t - start32(p, t));
-        ref = -slope2 * (visible32(p, t, lm) > 0 ? fmaxf(entry_distance(t, 0, p.m), first) : first);
-      }
+      // What the row's distances are relative to: 0 where near keys lead, the farthest key's where far ones do.
+      const float far = slope2 < 0.f && t >= 0 ? far_distance(t, start32(p, t), 0, p.m, p.n_win) : 0.f;
+      const float ref = -slope2 * far;  // kBounded: the reference
+      float negref = 0.f;  // otherwise what is added to the row's logits: their reference so far, with the other sign
       {
         const Segment& sg = d.seg;
         // this row's keys in the segment's list: window lo .. hi - 1, entries n_w .. end - 1
@@ -773,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           hi = t - sg.wlo + 1;
           end = n_w + visible32(p, t, lm);
           shift = t - sg.thi;
+          if (MODE != kBounded && slope2 < 0.f) negref = slope2 * (far - static_cast<float>(shift));
         }
         for (int k = 0; k < ntiles; ++k, ++it) {
           const uint32_t gt = g + it;
@@ -825,8 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(sb, *reinterpret_cast<uint32_t(*)[32]>(s));
           tmem_ld32(sb + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
           tmem_ld_wait();
-          apply_rule<CAP>(s, reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf), r, slope2,
-                          m_used == -INFINITY ? 0.f : -m_used);
+          apply_rule<CAP>(s, reinterpret_cast<const float4*>(sPos + st * kNk + 64 * hf), r, slope2, negref);
           float mt = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -845,8 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mt = max3(mt, m0, m1);
           }
-          // The logits stand on the old maximum (0 before the row's first key).
-          const bool fresh = m_used == -INFINITY;
+          // The logits stand on the old maximum (the farthest key's bias, or 0, before the row's first key).
           const bool bad = !good || *sAbort != 0;
           if (named_sync_or(1 + w, kTileThreads, bad || mt > kRescaleThreshold || (fresh && mt != -INFINITY))) {
             *side = mt;
@@ -856,10 +854,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             mt = fmaxf(mt, *other);
             const bool up = mt > kRescaleThreshold || (fresh && mt != -INFINITY);
-            const float delta = up ? mt : 0.f;
-            const float corr = up ? (fresh ? 0.f : ex2(-mt)) : 1.f;
+            // the step that negref takes, which may be a coarse one, not mt itself: every logit gets the same
+            const float delta = up ? negref - (negref - mt) : 0.f;
+            const float corr = up ? (fresh ? 0.f : ex2(-delta)) : 1.f;
             l_run *= corr;
-            if (up) m_used = fresh ? mt : m_used + mt;
+            if (up) {
+              negref -= mt;
+              fresh = false;
+            }
 #pragma unroll
             for (int j = 0; j < 64; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) - delta);
             if (it > 0) {
@@ -900,15 +902,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MODE == kBounded) {
         l_a = __fadd2_rn(l_a, l_b);
         l_run = l_a.x + l_a.y;
-        m_used = ref;
-      } else {
-        m_used -= slope2 * static_cast<float>(shift);
       }
       ok = !fail && __all_sync(kFull, n_item == 0 || mbar_wait(&lfree[w], (n_item - 1) & 1u, p.status));
       if (MODE != kBounded) ok = !named_sync_or(1 + w, kTileThreads, !ok);
       if (!ok) break;
       sSum[(2 * w + hf) * kTileRows + tr] = l_run;
-      if (hf == 0) sBase[w * kTileRows + tr] = m_used;
+      if (hf == 0) sBase[w * kTileRows + tr] = MODE == kBounded ? ref : -negref - slope2 * static_cast<float>(shift);
       __syncwarp();
       if (lane == 0) mbar_arrive(&lready[w]);
       item_done(n_item);

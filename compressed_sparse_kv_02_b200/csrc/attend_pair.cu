@@ -74,7 +74,8 @@ struct Smem {
   static constexpr int P = K + kNS * kStageBytes;
   static constexpr int ROWS = P + 2 * kPBytes;    // [2] source-row codes of the tile being issued, and the last one's
   static constexpr int DIST = ROWS + 2 * kRows * 4;  // RULE: minus the distances [stage][query][64 keys]
-  static constexpr int BAR = DIST + kNS * 2 * kNk * 4;
+  static constexpr int BIAS = DIST + kNS * 2 * kNk * 4;  // RULE: [256 softmax threads] slope and reference of a row
+  static constexpr int BAR = BIAS + 256 * 8;
   static constexpr int TMEM = BAR + (2 * kNS + 9) * 8;
   static constexpr int FLAGS = TMEM + 4;
   static constexpr int MASK = FLAGS + 8;          // valid-key bits: [stage][query][2 words]
@@ -83,7 +84,7 @@ struct Smem {
   static constexpr size_t bytes() { return 1024 + END; }
 };
 static_assert(Smem::bytes() <= 232448, "shared memory budget");
-static_assert(Smem::DIST % 16 == 0 && Smem::BAR % 8 == 0 && Smem::MASK % 4 == 0, "alignment");
+static_assert(Smem::DIST % 16 == 0 && Smem::BAR % 8 == 0 && Smem::MASK % 4 == 0 && Smem::BIAS % 8 == 0, "alignment");
 
 // source-row code: kind in bits [31:30] (0 none, 1 pool entry, 2 ring row, 3 chunk row), row below
 constexpr uint32_t kRowBits = 30;
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
   uint32_t* sMask = reinterpret_cast<uint32_t*>(sm + Smem::MASK);
   float* sDist = reinterpret_cast<float*>(sm + Smem::DIST);
   float* sSide = reinterpret_cast<float*>(sm + Smem::SIDE);
+  float2* sBias = reinterpret_cast<float2*>(sm + Smem::BIAS);
 
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
@@ -270,6 +272,13 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
   if (blockIdx.x == 0)
     for (int b = tid; b < p.n_q; b += kThreads)
       if (p.q_pos[b] < 0 || p.q_pos[b] > p.max_pos) report(p.status, CSKV_ERR_INVALID_ARG);
+
+  if (RULE && (warp < 4 || warp >= kSecondWarp0)) {
+    // A softmax thread's slope and what its row's logits are relative to: the bias of the farthest key, where the slope
+    // is negative. In shared memory, each thread its own, they cost no register in the loops.
+    const int qd = warp & 3, hf = warp >= kSecondWarp0;
+    sBias[hf * 128 + qd * 32 + lane] = make_float2(p.slopes ? p.slopes[qd * 16 + (lane & 15)] * kLog2e : 0.f, 0.f);
+  }
 
   const int n_items = (p.n_q + 1) >> 1;
   uint32_t g = 0;       // tiles of this CTA before the current item
@@ -520,7 +529,12 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
       const int qd = warp & 3, hf = warp >= kSecondWarp0;  // quarter of tensor memory (a warp reads that of its number)
       const int slot = lane >> 4, h = qd * 16 + (lane & 15), row = qd * 32 + lane;
       const int b_mine = slot ? b1 : b0;
-      const float slope2 = p.slopes ? p.slopes[h] * kLog2e : 0.f;
+      float2* bias = sBias + hf * 128 + row;
+      if (bias->x < 0.f) {  // far keys lead
+        const Keys km = slot ? k1 : k0;
+        const int64_t j = km.n == km.n_w ? -1 : p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b_mine * p.k]) : 0;
+        bias->y = bias->x * far_distance(km.t, km.ws, j, p.m, p.n_win);
+      }
       const uint32_t trow = tmem + (static_cast<uint32_t>(qd * 32) << 16);
       uint8_t* prow = sP + slot * (kPBytes / 2) + h * 128;
       const int sw = h & 7;
@@ -540,10 +554,11 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
           tmem_ld32(trow + kColS + (gt & 1u) * kNk + 32 * hf, s);
           tmem_ld_wait();
           const float4* pos = reinterpret_cast<const float4*>(sDist + st * kRows + slot * kNk + 32 * hf);
+          const float2 sb = *bias;
           if (rule.cap2.x > 0.f)
-            apply_rule<true>(s, pos, rule, slope2, 0.f);
+            apply_rule<true>(s, pos, rule, sb.x, sb.y);
           else
-            apply_rule<false>(s, pos, rule, slope2, 0.f);
+            apply_rule<false>(s, pos, rule, sb.x, sb.y);
           const uint32_t vm = sMask[st * 4 + slot * 2 + hf];
           if (!__all_sync(kFull, vm == kFull)) {
 #pragma unroll
@@ -658,7 +673,7 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
         }
       }
       if (hf == 0 && write && p.lse)
-        p.lse[(int64_t)b_mine * p.n_heads + h] = has ? (m_used + log2f(l_run)) * kLn2 : -INFINITY;
+        p.lse[(int64_t)b_mine * p.n_heads + h] = has ? (m_used + log2f(l_run)) * kLn2 - bias->y * kLn2 : -INFINITY;
       tc_fence_before();  // the next item's first P V overwrites O: this thread's reads of it are complete
     } else if constexpr (!RULE) {
       // ---------------------------------------------------------------- softmax (one head row per thread)

@@ -704,6 +704,13 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
       const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
       const int hr = warp * 16 + (lane & 15), kh = lane >> 4;
       const float slope2 = RULE && p.slopes ? p.slopes[grp * kH + hr] * kLog2e : 0.f;
+      // a negative slope's logits are relative to the bias of the row's farthest key (no branch on the slope: its load
+      // is waited for at the first softmax)
+      float negref = 0.f;
+      if (RULE && p.slopes) {
+        const int64_t j = kk.n == kk.n_w ? -1 : p.is_csa ? static_cast<int64_t>(p.sel_idx[(int64_t)b * p.k]) : 0;
+        negref = fminf(slope2, 0.f) * far_distance(kk.t, kk.ws, j, p.m, p.n_win);
+      }
       uint8_t* prow = sP + hr * 128;
       float m_used = -INFINITY, l_run = 0.f;
       bool ok = true;
@@ -753,9 +760,9 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) u[j] = __float_as_uint(s[j]);
             if (rule.cap2.x > 0.f)
-              apply_rule<true>(u, pos, rule, slope2, 0.f);
+              apply_rule<true>(u, pos, rule, slope2, negref);
             else
-              apply_rule<false>(u, pos, rule, slope2, 0.f);
+              apply_rule<false>(u, pos, rule, slope2, negref);
 #pragma unroll
             for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(u[j]);
           }
@@ -880,10 +887,10 @@ __global__ void __launch_bounds__(Block<FP8>::kThreads, 1)
       }
       if (kh == 0) {
         const float lse = l_row > 0.f ? (m_used + log2f(l_row)) * kLn2 : -INFINITY;
-        if (!whole)
-          p.part_lse[slot * p.n_heads + head] = lse;
-        else if (p.lse)
-          p.lse[(int64_t)b * p.n_heads + head] = lse;
+        if (!whole) p.part_lse[slot * p.n_heads + head] = lse;
+        // pieces are relative: the first leaves the reference where the merge looks for it
+        if (RULE && p.lse && (whole || (split == 0 && p.slopes)))
+          p.lse[(int64_t)b * p.n_heads + head] = whole ? lse - negref * kLn2 : -negref * kLn2;
       }
     }
     g += ntiles;

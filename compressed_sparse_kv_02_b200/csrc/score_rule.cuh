@@ -41,6 +41,15 @@ __device__ __forceinline__ float ruled_score(float s, float pre, float cap2, flo
 __device__ __forceinline__ float entry_distance(int64_t t, int64_t j, int m) {
   return 0.5f * static_cast<float>(2 * (t - j * m) - (m - 1));
 }
+// Under a negative slope far keys lead, with a bias whose fp32 step is coarse (1/16 in log2 units at slope -1/2 and 1M
+// tokens). Such a row's logits are therefore taken relative to the bias of its farthest key, whose distance this is:
+// `first` is the window's first position, j the row's first entry (below 0 or not visible: none). Entry 0 stands at
+// the middle of its block, so while the window begins before that its first token is the farther one. Any other key
+// would do as well for the answer, at the price of a coarser step.
+__device__ __forceinline__ float far_distance(int64_t t, int64_t first, int64_t j, int m, int n_win) {
+  const float w = static_cast<float>(t - first);
+  return j >= 0 && j * m < t + 1 - n_win ? fmaxf(entry_distance(t, j, m), w) : w;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -154,7 +163,7 @@ __device__ __forceinline__ void rule_n(uint32_t (&s)[N], const float4* pos, cons
 }
 
 // The rule on N logits of a row, in place: pos holds each key's position relative to some reference of the row's, and
-// negref what is added to every logit.
+// negref what is added to every logit (before the rounding of the bias: slope2 * pos is exact inside the sum).
 template <bool CAP, int N>
 __device__ __forceinline__ void apply_rule(uint32_t (&s)[N], const float4* pos, const Rule& r, float slope2,
                                            float negref) {

@@ -147,3 +147,28 @@ def test_a_missing_first_page_under_a_negative_slope(ck, cap, H, n_q):
     out, lse = s.run(cap, slopes, want=ck.ERR_OUT_OF_RANGE)
     s.L.page_table[0, 0] = page
     s.check(out, lse, cap, slopes, range(0, n_q, max(1, n_q // 20)))
+
+
+# every kernel: split (HCA in pieces, CSA, FP8), latent (bf16, FP8, one piece and several), query pairs, chunk
+FAR = [("hca", 128, 128, 32, 3, False, 0), ("csa", 128, 128, 16, 3, False, 0), ("csa", 128, 128, 32, 2, True, 0),
+       ("hca", 576, 512, 64, 3, False, 0), ("csa", 576, 512, 128, 3, False, 0), ("csa", 576, 512, 64, 3, True, 0),
+       ("csa", 576, 512, 64, 160, False, 0), ("csa", 128, 128, 64, 600, False, 0), ("hca", 128, 128, 64, 600, False, 32),
+       ("hca", 128, 128, 64, 600, False, 0), ("hca", 128, 128, 48, 600, False, 0)]
+
+
+@pytest.mark.parametrize("kind,d_qk,d_v,H,n_q,fp8,rope", FAR)
+@pytest.mark.parametrize("cap", [0.0, 50.0, 400.0])
+def test_negative_slopes_over_long_distances(ck, kind, d_qk, d_v, H, n_q, fp8, rope, cap):
+    """Far keys lead by biases of up to 5e5, whose fp32 step alone would be several percent of a weight: the logits that
+    count are small beside each other. (The bound allows for biases up to 100 below the leading key's.)"""
+    pos = [(1 << 20) - 1 - i for i in range(n_q)][::-1]
+    s = Setup(ck, kind, d_qk, d_v, H, [0] * n_q, pos, k=96 if kind == "csa" else 0, fp8=fp8, seed=H + n_q,
+              chunk={0: (0, pos[0], n_q)} if n_q > 160 else None, q_std=2.0 if kind == "csa" else 16.0)
+    if s.k:  # neighbours among the far entries, so that several of them have a weight
+        s.sel[:, :64] = torch.arange(3, 67, device="cuda")
+        s.sel[:, 64:] = s.sel[:, 64:].clamp(min=1000).sort(1).values
+    slopes = -torch.exp2(torch.linspace(-9, -1, H, device="cuda"))
+    slopes[1::5] = 2.0 ** -8  # some heads look near
+    out, lse = s.run(cap, slopes, rope_dims=rope)
+    some = sorted({0, 1, n_q // 2, n_q - 1})
+    s.check(out, lse, cap, slopes, some, rope=rope)
