@@ -29,7 +29,7 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// cuTensorMapEncodeTiled, looked up once through the runtime (null if unavailable)
+// cuTensorMapEncodeTiled, looked up once through the runtime, with a context current (null if unavailable)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // One stream of raw tokens folded into compressed entries (the latent-KV

@@ -1687,17 +1687,28 @@ cudaError_t launch_select_stream(IndexParams& p, cudaStream_t st) {
 
 }  // namespace
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link)
+// Driver calls through the runtime's entry points (no libcuda link). A host thread whose first CUDA work this call is
+// has no context yet, and the driver, unlike the runtime, does not make the current device's one current by itself: the
+// encoder would refuse every map.
+namespace {
+template <typename F>
+F driver_entry(const char* name) {
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint(name, &f, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<F>(f);
+}
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
+  static const auto encode = driver_entry<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
+  static const auto current = driver_entry<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent");
+  CUcontext ctx = nullptr;
+  int dev = 0;
+  if (!current || current(&ctx) != CUDA_SUCCESS) return nullptr;
+  if (!ctx && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)) return nullptr;
+  return encode;
 }
 
 size_t index_ws_bytes(int n_q, int64_t max_pos, int m, int n_win) {
