@@ -535,7 +535,7 @@ template <int DQK, int DV, int MT, int VS, bool FP8, bool RULE>
 cudaError_t run_attend_form(AttendParams& p, int n_sm, cudaStream_t st) {
   auto kern = attend_kernel<DQK, DV, MT, VS, FP8, RULE>;
   const size_t smem = AttnSmem<DQK, MT>::bytes(p.n_q, p.keys_per_split, FP8, RULE);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem, 32 * sizeof(int));  // s_wsum
   if (e != cudaSuccess) return e;
   int per_sm = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * MT * VS, smem);

@@ -982,8 +982,7 @@ cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st) {
   const size_t smem = smem_bytes(fp8, rule, p.n_q);
   auto kern = rule ? (fp8 ? attend_tc_kernel<true, true> : attend_tc_kernel<false, true>)
                    : (fp8 ? attend_tc_kernel<true, false> : attend_tc_kernel<false, false>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem, 32 * sizeof(int));  // s_wsum
   if (e != cudaSuccess) return e;
   const int64_t groups = p.n_heads / kH;
   const int64_t items = (int64_t)p.n_q * p.max_splits * groups;

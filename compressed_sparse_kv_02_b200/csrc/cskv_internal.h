@@ -29,6 +29,16 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Lets `kern` be launched with `smem` bytes of dynamic shared memory, which vary from call to call. The limit set is
+// always the largest one that leaves the kernel's `fixed` static bytes: two host threads may be between this call and
+// their launches at once, and neither may lower the other's limit.
+constexpr size_t kBlockSmem = 232448;  // of a block at most
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, size_t smem, size_t fixed) {
+  if (smem + fixed > kBlockSmem) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBlockSmem - fixed));
+}
+
 // cuTensorMapEncodeTiled, looked up once through the runtime, with a context current (null if unavailable)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 

@@ -1426,7 +1426,7 @@ cudaError_t launch_scan_tma(IndexParams& p, int n_sm, cudaStream_t st) {
   }
   auto kern = index_scan_tma_kernel<NCH, NTH, FP4>;
   const size_t smem = TmaScanShape<NCH, FP4>::smem_bytes(p.n_q);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem, sizeof(int) * 32 + 2 * sizeof(uint32_t) * kHistBins);  // s_wsum, s_h
   if (e != cudaSuccess) return e;
   const int64_t units_max = (visible_entries(p.max_pos, p.m, p.n_win) + kUnitKeys - 1) / kUnitKeys;
   int64_t grid = units_max * p.n_q;
@@ -1451,7 +1451,7 @@ cudaError_t launch_scan_group(IndexParams& p, int n_sm, cudaStream_t st) {
   auto kern = index_scan_group_kernel<NCH, HI>;
   const size_t smem = 1024 + (size_t)kTmaRingBytes + 2 * TmaScanShape<NCH>::NSTAGE * sizeof(uint64_t) +
                       TmaScanShape<NCH>::NSTAGE * sizeof(int) + 2 * sizeof(int) * (size_t)(p.n_q + 1);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem, sizeof(int) * 36);  // s_wsum, s_nent
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(n_sm)), dim3(kTmaThreads), smem, st, map, p);
 }

@@ -364,7 +364,7 @@ cudaError_t run_scan_tc(IndexParams& p, int n_sm, cudaStream_t st) {
   auto kern = index_scan_tc_kernel<KB, HI>;
   const size_t smem = TcScan<KB>::bytes(p.n_q);
   if (smem > 232448) return cudaErrorNotSupported;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_smem(kern, smem, sizeof(int) * 36);  // s_wsum, s_nent
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(n_sm)), dim3(kTcThreads), smem, st, tm_k, tm_q, p);
 }

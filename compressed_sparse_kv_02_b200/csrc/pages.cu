@@ -430,7 +430,7 @@ cudaError_t launch_reserve(const PageParams& p, void* ws, int n_sm, cudaStream_t
   const size_t smem = sizeof(int) * (3 * (size_t)p.n + 1);
   cudaError_t e = cudaSuccess;
   if (smem > 40000)  // the static default is 48 KB, the kernel's own arrays included
-    e = cudaFuncSetAttribute(reserve_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = allow_smem(reserve_plan_kernel, smem, 32 * sizeof(int));
   if (e != cudaSuccess) return e;
   e = launch_pdl(reserve_plan_kernel, dim3(1 + rank_ctas(p.n_pages)), dim3(kRankThreads), smem, st, p, w);
   if (e != cudaSuccess) return e;

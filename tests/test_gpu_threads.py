@@ -1,4 +1,5 @@
-"""GPU test of calls from several host threads."""
+"""GPU tests of calls from several host threads: a thread's first call, and calls of two sizes at once."""
+import ctypes
 import threading
 
 import pytest
@@ -76,3 +77,73 @@ def test_first_call_of_a_thread(ck, make):
     torch.cuda.synchronize()
     assert not bad, bad
     assert torch.equal(out, want)
+
+
+def _raw_reserve(ck, n, stream):
+    """cskv_cache_reserve of n sequences without new pages, through the C ABI: as little Python between calls as possible."""
+    from compressed_sparse_kv_02_b200 import _binding as b
+    L = ck.Layer.allocate(ck.LAYER_HCA, 128, 16, 16, 4096, 64, 4, page_size=16, gate_cols=1)
+    L.track_pages()
+    seqs, zero = torch.arange(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int64, device="cuda")
+    ws, s = torch.empty(ck.cskv_reserve_ws_bytes(L, n, 1), dtype=torch.uint8, device="cuda"), L.struct
+    a = b.ReserveArgs(ctypes.sizeof(b.ReserveArgs), ctypes.pointer(s), L.page_refs.data_ptr(), n, seqs.data_ptr(),
+                      zero.data_ptr(), zero.data_ptr(), 1, None)
+    return ck.lib().cskv_cache_reserve, a, ws, stream, (L, seqs, zero, s)
+
+
+def _raw_attend(ck, n, stream, d_qk, d_v, H, cap):
+    from compressed_sparse_kv_02_b200 import _binding as b
+    L = ck.Layer.allocate(ck.LAYER_HCA, 128, d_qk, d_v, 1, 8, 8, gate_cols=1)
+    L.set_pages(0, torch.arange(8))
+    q, out = (torch.zeros(n, H, d, dtype=torch.bfloat16, device="cuda") for d in (d_qk, d_v))
+    seq, pos = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.zeros(n, dtype=torch.int64, device="cuda")
+    ws = torch.empty(ck.cskv_attend_ws_bytes(L, n, H, 700), dtype=torch.uint8, device="cuda")
+    a = b._attend_args(L, seq, pos, 700, q, None, None, 0, None, out, None, None, 0, None, score_cap=cap)
+    return ck.lib().hca_attend, a, ws, stream, (L, q, out, seq, pos)
+
+
+def _raw_select(ck, n, stream):
+    from compressed_sparse_kv_02_b200 import _binding as b
+    L = ck.Layer.allocate(ck.LAYER_CSA, 4, 128, 128, 1, 8, 8, d_idx=64, gate_cols=1, gate_cols_idx=1)
+    L.set_pages(0, torch.arange(8))
+    w, qi = torch.zeros(n, 4, device="cuda"), torch.zeros(n, 4, 64, dtype=torch.bfloat16, device="cuda")
+    seq, pos = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.full((n,), 500, dtype=torch.int64, device="cuda")
+    idx, cnt = torch.zeros(n, 64, dtype=torch.int32, device="cuda"), torch.empty(n, dtype=torch.int32, device="cuda")
+    ws = torch.empty(ck.csa_index_ws_bytes(L, n, 4, 500, 64), dtype=torch.uint8, device="cuda")
+    a = b._index_args(L, seq, pos, 500, qi, w, 64, idx, cnt, None, None, None)
+    return ck.lib().csa_index_score_topk, a, ws, stream, (L, w, qi, seq, pos, idx, cnt)
+
+
+@pytest.mark.parametrize("make,sizes,times", [
+    (_raw_reserve, (3400, 4096), 500),
+    (lambda ck, n, s: _raw_attend(ck, n, s, 128, 128, 32, 0.0), (1, 400), 8000),
+    (lambda ck, n, s: _raw_attend(ck, n, s, 128, 128, 32, 30.0), (1, 400), 8000),
+    (lambda ck, n, s: _raw_attend(ck, n, s, 576, 512, 64, 0.0), (1, 170), 8000),
+    (lambda ck, n, s: _raw_attend(ck, n, s, 576, 512, 64, 30.0), (1, 170), 8000),
+    (lambda ck, n, s: _raw_attend(ck, n, s, 576, 512, 64, 30.0), (300, 900), 4000),
+    (_raw_select, (1, 10), 4000), (_raw_select, (40, 63), 4000), (_raw_select, (700, 900), 4000)],
+    ids=["reserve", "split", "split rule", "latent", "latent rule", "latent split", "scan", "scan group", "scan tc"])
+def test_calls_of_two_sizes_at_once(ck, make, sizes, times):
+    """Two threads on streams and buffers of their own: a kernel's limit on dynamic shared memory is the process's, so a
+    smaller call may not lower it between the other's setting it and its launch."""
+    streams = [torch.cuda.Stream() for _ in sizes]
+    made = [make(ck, n, s) for n, s in zip(sizes, streams)]
+    torch.cuda.synchronize()
+    gate, failed = threading.Barrier(len(sizes)), [0] * len(sizes)
+
+    def work(i):
+        f, a, ws, stream, _ = made[i]
+        p, w, n, st = ctypes.byref(a), ws.data_ptr(), ws.numel(), ctypes.c_void_p(stream.cuda_stream)
+        gate.wait(60)
+        for k in range(times):
+            failed[i] += f(p, w, n, st) != ck.OK
+            if k % 500 == 499:
+                stream.synchronize()
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0] * len(sizes)
