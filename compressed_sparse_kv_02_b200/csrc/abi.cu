@@ -316,10 +316,12 @@ cskv_status check_compact(const cskv_compact_args* a) {
   cskv_status s = check_paged(a->src);
   if (s || (s = check_paged(a->dst))) return s;
   const cskv_layer &x = *a->src, &y = *a->dst;
-  if (x.kind != y.kind || x.page_size != y.page_size || x.d_qk != y.d_qk || x.kv_dtype != y.kv_dtype ||
+  if (x.kind != y.kind || x.m != y.m || x.n_win != y.n_win || x.page_size != y.page_size || x.d_qk != y.d_qk ||
+      x.d_v != y.d_v || x.kv_dtype != y.kv_dtype || x.gate_cols != y.gate_cols || layer_overlap(a->src) != layer_overlap(a->dst) ||
       x.n_seqs != y.n_seqs || y.max_pages_per_seq < x.max_pages_per_seq)
     return CSKV_ERR_INVALID_ARG;
-  if (x.kind == CSKV_LAYER_CSA && (x.d_idx != y.d_idx || x.idx_dtype != y.idx_dtype)) return CSKV_ERR_INVALID_ARG;
+  if (x.kind == CSKV_LAYER_CSA && (x.d_idx != y.d_idx || x.idx_dtype != y.idx_dtype || x.gate_cols_idx != y.gate_cols_idx))
+    return CSKV_ERR_INVALID_ARG;
   return CSKV_OK;
 }
 
