@@ -472,12 +472,17 @@ cskv_status cskv_cache_compact(const cskv_compact_args* a, void* ws, size_t ws_b
   if (!fill_pages(src, a->src, const_cast<int32_t*>(a->src_refs), a->d_status) ||
       !fill_pages(dst, a->dst, a->dst_refs, a->d_status))
     return CSKV_ERR_INVALID_ARG;
-  for (int i = 0; i < 4; ++i)
-    if (overlap(src.pool[i].base, src.pool[i].bytes * src.n_pages, dst.pool[i].base, dst.pool[i].bytes * dst.n_pages))
-      return CSKV_ERR_INVALID_ARG;
-  if (overlap(src.refs, 4 * src.n_pages, dst.refs, 4 * dst.n_pages) ||
-      overlap(src.table, (int64_t)4 * src.n_seqs * src.max_pages, dst.table, (int64_t)4 * dst.n_seqs * dst.max_pages))
-    return CSKV_ERR_INVALID_ARG;
+  // what dst gets is written while src is read, so no buffer of the one may lie in any of the other
+  const auto buffers = [](const cskv::PageParams& p, int i, const void*& base) -> int64_t {
+    base = i < 4 ? p.pool[i].base : i == 4 ? static_cast<const void*>(p.refs) : p.table;
+    return i < 4 ? p.pool[i].bytes * p.n_pages : i == 4 ? 4 * p.n_pages : (int64_t)4 * p.n_seqs * p.max_pages;
+  };
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < 6; ++j) {
+      const void *x, *y;
+      const int64_t nx = buffers(src, i, x), ny = buffers(dst, j, y);
+      if (overlap(x, nx, y, ny)) return CSKV_ERR_INVALID_ARG;
+    }
   if (!ws || ws_bytes < cskv::compact_ws_bytes(src) || !aligned16(ws)) return CSKV_ERR_WORKSPACE;
   return from_cuda(cskv::launch_compact(src, dst, ws, sm_count(), static_cast<cudaStream_t>(stream)));
 }

@@ -35,3 +35,24 @@ def test_compact_ignores_what_an_hca_layer_does_not_use(ck, field, value):
     a = b.CompactArgs(ctypes.sizeof(b.CompactArgs), ctypes.pointer(x), ctypes.pointer(y), FAKE, FAKE * 2, None)
     n = ctypes.c_size_t()
     assert L.cskv_compact_ws_bytes(ctypes.byref(a), ctypes.byref(n)) == ck.OK
+
+
+@pytest.mark.parametrize("mine,others", [("kv_pool", "idx_pool"), ("idx_pool", "kv_pool"), ("kv_pool", "page_table"),
+                                         ("page_table", "kv_pool"), ("page_table", "refs"), ("refs", "idx_pool")])
+def test_compact_refuses_any_shared_buffer(ck, mine, others):
+    """A buffer of dst inside another one of src."""
+    L, b = ck.lib(), _b()
+    for shared in (True, False):
+        x, y = _struct(ck), _struct(ck, n_pages=400)
+        for f in ("page_table", "kv_pool", "idx_pool"):
+            setattr(y, f, getattr(y, f) + (1 << 44))
+        refs = {"x": FAKE, "y": FAKE * 2}
+        if shared:
+            at = (refs["x"] if others == "refs" else getattr(x, others)) + 32
+            if mine == "refs":
+                refs["y"] = at
+            else:
+                setattr(y, mine, at)
+        a = b.CompactArgs(ctypes.sizeof(b.CompactArgs), ctypes.pointer(x), ctypes.pointer(y), refs["x"], refs["y"], None)
+        want = ck.ERR_INVALID_ARG if shared else ck.ERR_WORKSPACE  # without a workspace nothing is launched
+        assert L.cskv_cache_compact(ctypes.byref(a), None, 1 << 30, None) == want
