@@ -201,12 +201,13 @@ __device__ __forceinline__ int64_t chunk_row(const AttendParams& p, int seq, int
     r0 = p.chunk_desc[3 * (int64_t)seq];
     p0 = p.chunk_desc[3 * (int64_t)seq + 1];
     len = p.chunk_desc[3 * (int64_t)seq + 2];
-    if (r0 < 0 || len < 0 || r0 + len > p.chunk_len) {
+    if (r0 < 0 || len < 0 || len > p.chunk_len || r0 > p.chunk_len - len) {  // (no sum that could pass 63 bits)
       if (p.status) atomicCAS(p.status, 0, CSKV_ERR_OUT_OF_RANGE);
       return -1;
     }
   }
-  return (pos >= p0 && pos < p0 + len) ? r0 + pos - p0 : -1;
+  const uint64_t at = static_cast<uint64_t>(pos) - static_cast<uint64_t>(p0);
+  return pos >= p0 && at < static_cast<uint64_t>(len) ? r0 + static_cast<int64_t>(at) : -1;
 }
 cudaError_t launch_attend(AttendParams& p, void* ws, int n_sm, cudaStream_t st);
 bool attend_supported(int d_qk, int d_v, int n_heads, int kv_dtype);

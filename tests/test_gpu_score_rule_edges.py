@@ -172,3 +172,36 @@ def test_negative_slopes_over_long_distances(ck, kind, d_qk, d_v, H, n_q, fp8, r
     out, lse = s.run(cap, slopes, rope_dims=rope)
     some = sorted({0, 1, n_q // 2, n_q - 1})
     s.check(out, lse, cap, slopes, some, rope=rope)
+
+
+BIG = (1 << 63) - 1
+
+
+@pytest.mark.parametrize("kind,d_qk,d_v,H,n_q,fp8", [("hca", 128, 128, 32, 4, False), ("csa", 576, 512, 64, 5, True),
+                                                      ("hca", 576, 512, 64, 5, False), ("csa", 128, 128, 64, 640, False),
+                                                      ("hca", 128, 128, 64, 700, False)])
+@pytest.mark.parametrize("desc,outside", [((BIG, 1500, 1), True), ((1, 1500, BIG), True), ((-1, 1500, 2), True),
+                                          ((0, 1500, -1), True), ((BIG - 5, 1500, 6), True), ((4, 1500, 100000), True),
+                                          ((0, BIG, 2), False), ((0, -BIG - 1, 2), False), ((0, -BIG - 1 + 1500, 1), False)])
+@pytest.mark.parametrize("cap", [30.0, 70.0])
+def test_descriptors_of_any_value(ck, kind, d_qk, d_v, H, n_q, fp8, desc, outside, cap):
+    """A chunk descriptor outside x_chunk, its sums past 63 bits among them, is reported and its rows come from the ring;
+    positions far from every query's name none of them."""
+    pos = list(range(1500, 1500 + n_q))
+    s = Setup(ck, kind, d_qk, d_v, H, [0] * n_q, pos, k=64 if kind == "csa" else 0, fp8=fp8, seed=2, chunk={1: (0, 0, n_q)})
+    from compressed_sparse_kv_02_b200 import _binding as b
+    import ctypes
+    out = torch.full((n_q, H, d_v), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n_q, H), 7.0, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    d = torch.zeros(s.L.n_seqs, 3, dtype=torch.int64)
+    d[0] = torch.tensor(desc)
+    d = d.cuda()
+    ws = torch.empty(ck.cskv_attend_ws_bytes(s.L, n_q, H, max(pos), s.k), dtype=torch.uint8, device="cuda")
+    a = b._attend_args(s.L, s.q_seq, s.q_pos, max(pos), s.q, s.sel if s.k else None, s.cnt if s.k else None, s.k, None,
+                       out, lse, s.x_chunk, 0, st, chunk_desc=d, score_cap=cap, slopes=s.slopes)
+    f = ck.lib().csa_attend if s.k else ck.lib().hca_attend
+    assert f(ctypes.byref(a), ws.data_ptr(), ws.numel(), b._stream(None)) == ck.OK
+    assert ck.cskv_get_status(st) == (ck.ERR_OUT_OF_RANGE if outside else ck.OK)
+    s.chunk = None  # every window row is the ring's
+    s.check(out, lse, cap, s.slopes, sorted({0, n_q // 2, n_q - 1}))
