@@ -190,6 +190,10 @@ cskv_status check_attend(const cskv_attend_args* a, int kind) {
   if (a->n_q < 0 || a->n_heads < 1 || a->max_pos < 0) return CSKV_ERR_INVALID_ARG;
   if (kind == CSKV_LAYER_CSA && a->k < 1) return CSKV_ERR_INVALID_ARG;
   if (!(a->sm_scale > 0.f)) return CSKV_ERR_INVALID_ARG;
+  if (has_rule_fields(a) && a->score_cap != 0.f) {  // the cap's arithmetic is on sm_scale / score_cap
+    const float r = a->sm_scale / a->score_cap;
+    if (!(r >= 0x1p-120f && r <= 0x1p120f)) return CSKV_ERR_INVALID_ARG;
+  }
   if (!cskv::attend_supported(L->d_qk, L->d_v, a->n_heads, L->kv_dtype)) return CSKV_ERR_UNSUPPORTED;
   if (a->n_q > 4096) return CSKV_ERR_UNSUPPORTED;
   return CSKV_OK;

@@ -51,8 +51,6 @@
 // row would turn into NaN. A row whose output is not finite is therefore taken again
 // by its warp from its own keys only (slow_row), so that no key outside a query's
 // own set can reach its answer.
-#include <float.h>
-
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"

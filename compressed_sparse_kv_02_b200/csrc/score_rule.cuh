@@ -1,6 +1,7 @@
 // score_rule.cuh -- the rule on attention logits (cap and distance bias) shared by the attention kernels.
 #pragma once
 
+#include <float.h>
 #include <stdint.h>
 
 namespace cskv {
@@ -80,6 +81,11 @@ struct Rule {
   float2 c[6];
   float lim;         // |s| up to here takes the polynomial (negative: never)
 };
+// The coefficients span pre^11, so with a scale far from 1 the last ones leave fp32's range. Above it the rational form
+// is taken for every logit. Below it (caps above ~430 at the usual scales) they are left out, and the polynomial is taken
+// where the first one left out would add less than 2^-24 of the sum: |u| <= kTanhU[m] with m coefficients, the 2m-th root of
+// 2^-24 / |kTanhP[m]|. s^2 has to stay in range as well, which 2^60 keeps it.
+constexpr float kTanhU[7] = {0.f, 4.2e-4f, 0.0258f, 0.102f, 0.208f, 0.337f, 1.f};
 inline Rule make_rule(float sm_scale, float score_cap) {
   const float log2e = 1.4426950408889634f;
   const bool cap = score_cap > 0.f;
@@ -87,12 +93,18 @@ inline Rule make_rule(float sm_scale, float score_cap) {
   const float pre = cap ? sm_scale / score_cap : sm_scale * log2e, cap2 = cap ? score_cap * log2e : 0.f;
   r.pre = make_float2(pre, pre);
   r.cap2 = make_float2(cap2, cap2);
-  r.lim = pre < 2048.f ? 1.f / pre : -1.f;  // above that pre^10 would leave fp32's range
+  int kept = 0;
+  bool fits = pre < 2048.f;
   float f = cap2 * pre;
   for (int i = 0; i < 6; ++i) {
-    r.c[i] = make_float2(f * kTanhP[i], f * kTanhP[i]);
+    if (kept == i && f >= 0x1p-125f) kept = i + 1;
+    const float c = kept > i ? f * kTanhP[i] : 0.f;
+    r.c[i] = make_float2(c, c);
+    fits = fits && f <= FLT_MAX;
     f *= pre * pre;
   }
+  const float lim = kTanhU[kept] / pre;
+  r.lim = !fits ? -1.f : lim < 0x1p60f ? lim : 0x1p60f;
   return r;
 }
 

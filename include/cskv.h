@@ -454,8 +454,9 @@ cskv_status csa_index_score_topk_static(const cskv_index_args* args, void* strea
  *   score_cap, slopes: a rule on the logits, for models trained with capped
  *     scores or with a distance bias instead of rotary positions:
  *       s(h, u) = cap tanh(sm_scale q.k / cap) - slopes[h] (t - p_u)
- *     score_cap = 0: no cap, else 2^-100 .. 2^100 (CSKV_ERR_INVALID_ARG outside,
- *     where the fp32 arithmetic would overflow); slopes [n_heads] fp32 or NULL: no bias (any sign,
+ *     score_cap = 0: no cap, else 2^-100 .. 2^100, and sm_scale / score_cap in
+ *     2^-120 .. 2^120 (CSKV_ERR_INVALID_ARG outside, where the fp32 arithmetic
+ *     would leave its range); slopes [n_heads] fp32 or NULL: no bias (any sign,
  *     finite, slope x distance within fp32's range; distances are exact below 2^23 tokens). p_u is a window token's position, and the mean position
  *     j m + (m - 1) / 2 of the tokens of entry j's own block: a bias that is
  *     linear in the position averages to its value there. lse is that of s.

@@ -205,3 +205,30 @@ def test_descriptors_of_any_value(ck, kind, d_qk, d_v, H, n_q, fp8, desc, outsid
     assert ck.cskv_get_status(st) == (ck.ERR_OUT_OF_RANGE if outside else ck.OK)
     s.chunk = None  # every window row is the ring's
     s.check(out, lse, cap, s.slopes, sorted({0, n_q // 2, n_q - 1}))
+
+
+@pytest.mark.parametrize("kind,d_qk,d_v,H,n_q", [("hca", 128, 128, 32, 4), ("csa", 576, 512, 64, 5),
+                                                 ("csa", 128, 128, 64, 640), ("hca", 128, 128, 64, 700)])
+@pytest.mark.parametrize("power,cap", [(60, 2.0 ** 20), (60, 2.0 ** 30), (-22, 190.0), (-30, 30.0), (30, 30.0)])
+def test_scales_far_from_one(ck, kind, d_qk, d_v, H, n_q, power, cap):
+    """Queries times 2^power with sm_scale times 2^-power: the same scores, from products far from one."""
+    pos = list(range(2000, 2000 + n_q))
+    s = Setup(ck, kind, d_qk, d_v, H, [0] * n_q, pos, k=64 if kind == "csa" else 0, seed=4, chunk={0: (0, 2000, n_q)})
+    q = s.q
+    s.q = q * 2.0 ** power
+    out, lse = s.run(cap, s.slopes, sm_scale=2.0 ** -power / d_qk ** 0.5)
+    s.q = q
+    s.check(out, lse, cap, s.slopes, sorted({0, n_q // 2, n_q - 1}))
+
+
+@pytest.mark.parametrize("kind,d_qk,d_v,H,n_q", [("hca", 128, 128, 32, 4), ("csa", 576, 512, 64, 5),
+                                                 ("csa", 128, 128, 64, 640), ("hca", 128, 128, 64, 700)])
+@pytest.mark.parametrize("cap", [300.0, 1000.0, 3000.0, 20000.0])
+def test_large_caps_within_reach(ck, kind, d_qk, d_v, H, n_q, cap):
+    """Scores of up to several times a large cap, and below it."""
+    pos = list(range(2000, 2000 + n_q))
+    for reach in (0.1, 0.5, 2.0):
+        s = Setup(ck, kind, d_qk, d_v, H, [0] * n_q, pos, k=64 if kind == "csa" else 0, seed=6, chunk={0: (0, 2000, n_q)},
+                  q_std=cap * reach / 4)
+        out, lse = s.run(cap, None)
+        s.check(out, lse, cap, None, sorted({0, n_q // 2, n_q - 1}))

@@ -47,3 +47,15 @@ def test_workspace_covers_the_split_kernel_behind_the_tensor_core_kernel(ck):
                      max_pages_per_seq=64, n_pages=512)
     sizes = [ck.cskv_attend_ws_bytes(layer, n, 64, 4000) for n in (100, 111, 112, 150, 175, 176, 300)]
     assert all(s > 0 for s in sizes)
+
+
+@pytest.mark.parametrize("sm_scale,cap", [(2.0 ** -30, 2.0 ** 100), (2.0 ** 40, 2.0 ** -90), (2.0 ** -121, 1.0), (3e38, 1.0)])
+def test_scales_beyond_the_cap_are_refused(ck, sm_scale, cap):
+    """sm_scale / score_cap outside 2^-120 .. 2^120."""
+    a = _args(ck, score_cap=cap)
+    a.sm_scale = sm_scale
+    n = ctypes.c_size_t()
+    assert ck.lib().cskv_attend_ws_bytes(ctypes.byref(a), ctypes.byref(n)) == ck.ERR_INVALID_ARG
+    assert ck.lib().hca_attend(ctypes.byref(a), None, 0, None) == ck.ERR_INVALID_ARG
+    a.score_cap = 0.0
+    assert ck.lib().cskv_attend_ws_bytes(ctypes.byref(a), ctypes.byref(n)) == ck.OK
