@@ -186,6 +186,15 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _temporary(n: int, device, stream) -> torch.Tensor:
+    """A workspace for one call on `stream`: it is not handed out again before the call has run, on whichever stream."""
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                         torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream), device=device))
+    return ws
+
+
 def _need(t: Optional[torch.Tensor], name: str, dtype, shape=None, optional=False):
     if t is not None and t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape):
         return
@@ -486,7 +495,7 @@ def cskv_cache_reserve(layer: Layer, seq_ids, first, count, max_count: int, work
     _need(count, "count", torch.int64, (n,))
     _need(status, "status", torch.int32, optional=True)
     if workspace is None:
-        workspace = torch.empty(cskv_reserve_ws_bytes(layer, n, max_count), dtype=torch.uint8, device=seq_ids.device)
+        workspace = _temporary(cskv_reserve_ws_bytes(layer, n, max_count), seq_ids.device, stream)
     s = layer.struct
     a = _packed(ReserveArgs, _RESERVE_PACK, ctypes.addressof(s), layer.page_refs.data_ptr(), n, seq_ids.data_ptr(),
                 first.data_ptr(), count.data_ptr(), int(max_count), _addr(status))
@@ -508,7 +517,7 @@ def cskv_cache_compact(src: Layer, dst: Layer, workspace=None, status=None, stre
     _need_refs(dst)
     _need(status, "status", torch.int32, optional=True)
     if workspace is None:
-        workspace = torch.empty(cskv_compact_ws_bytes(src, dst), dtype=torch.uint8, device=src.page_table.device)
+        workspace = _temporary(cskv_compact_ws_bytes(src, dst), src.page_table.device, stream)
     s, d = src.struct, dst.struct
     a = _packed(CompactArgs, _COMPACT_PACK, ctypes.addressof(s), ctypes.addressof(d), src.page_refs.data_ptr(),
                 dst.page_refs.data_ptr(), _addr(status))
@@ -553,8 +562,7 @@ def csa_index_score_topk(layer: Layer, q_seq, q_pos, max_pos: int, q_idx, w, k: 
     _need(out_scores, "out_scores", torch.float32, (n_q, k), optional=True)
     _need(status, "status", torch.int32, optional=True)
     if workspace is None:
-        workspace = torch.empty(csa_index_ws_bytes(layer, n_q, h_i, max_pos, k), dtype=torch.uint8,
-                                device=w.device)
+        workspace = _temporary(csa_index_ws_bytes(layer, n_q, h_i, max_pos, k), w.device, stream)
     a = _index_args(layer, q_seq, q_pos, max_pos, q_idx, w, k, out_idx, out_cnt, out_scores, q_idx_scale, status,
                     score_bf16)
     _check(lib().csa_index_score_topk(ctypes.byref(a), _ptr(workspace), workspace.numel(), _stream(stream)),
@@ -615,8 +623,7 @@ def _attend(fn, where, layer, q_seq, q_pos, max_pos, q, sel_idx, sel_cnt, k, out
     _need(x_chunk, "x_chunk", torch.bfloat16, optional=True)
     _need(status, "status", torch.int32, optional=True)
     if workspace is None:
-        workspace = torch.empty(cskv_attend_ws_bytes(layer, n_q, n_heads, max_pos, k), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _temporary(cskv_attend_ws_bytes(layer, n_q, n_heads, max_pos, k), q.device, stream)
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(layer.d_qk)
     s = layer.struct
