@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
 
   const int n_items = (p.n_q + 1) >> 1;
   uint32_t g = 0;       // tiles of this CTA before the current item
-  uint32_t n_item = 0;  // items of this CTA before the current one
-  for (int item = blockIdx.x; item < n_items && !__shfl_sync(kFull, *sAbort, 0); item += gridDim.x, ++n_item) {
+  uint32_t n_item = 0;  // items with keys of this CTA before the current one
+  for (int item = blockIdx.x; item < n_items && !__shfl_sync(kFull, *sAbort, 0); item += gridDim.x) {
     const int b0 = 2 * item, b1 = b0 + 1 < p.n_q ? b0 + 1 : -1;
     const Keys k0 = keys_of(p, b0);
     Keys k1;
@@ -314,6 +314,16 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
     ksh.n_vis = k1.n_vis;
     const int nmax = shared ? ksh.n : (n0 > n1 ? n0 : n1);
     const int ntiles = (nmax + kNk - 1) / kNk;
+    if (ntiles == 0) {
+      // Neither query has keys (padding): zeros and -inf. The item takes no part in the pipeline: with no tile to wait for,
+      // the MMA warp would run more than one phase of dbar ahead of the softmax, which would then wait for the wrong one.
+      const int n_out = b1 >= 0 ? 2 : 1;  // consecutive rows
+      uint4* out = reinterpret_cast<uint4*>(p.out + (int64_t)b0 * kH * kD);
+      for (int i = tid; i < n_out * kH * (kD / 8); i += kThreads) out[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int i = tid; i < n_out * kH; i += kThreads) p.lse[(int64_t)b0 * kH + i] = -INFINITY;
+      continue;
+    }
 
     if (tid >= kLoadThread0 && tid < kLoadThread0 + kLoaders) {
       // ---------------------------------------------------------------- loaders
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
       }
       load_q(true);
       cp_async_wait<0>();
-      if (ntiles > 0 && !*sAbort && !tma_before) {
+      if (!*sAbort && !tma_before) {
         fence_proxy_async_smem();
         mbar_arrive(&kfull[(g + ntiles - 1) % kNS]);
       }
@@ -517,7 +527,6 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
           __syncwarp();
         }
       }
-      if (nt == 0) commit_if(issuer, qempty);
       commit_if(issuer, dbar);  // one completion per item, also after an abort
       if (lane == 0 && !ok) *sAbort = 1;
       __syncwarp();
@@ -831,6 +840,7 @@ __global__ void __launch_bounds__(Block<RULE>::kThreads, 1)
       tc_fence_before();
     }
     g += ntiles;
+    ++n_item;
   }
   // after an abort, give tensor-core work and copies in flight a bounded chance to land (each
   // warp decides on lane 0's reading of the flag, so it stays converged)

@@ -232,3 +232,20 @@ def test_large_caps_within_reach(ck, kind, d_qk, d_v, H, n_q, cap):
                   q_std=cap * reach / 4)
         out, lse = s.run(cap, None)
         s.check(out, lse, cap, None, sorted({0, n_q // 2, n_q - 1}))
+
+
+@pytest.mark.parametrize("empty", list(EMPTY))
+@pytest.mark.parametrize("kind,d_qk,d_v,H,n,rope", [("csa", 128, 128, 64, 1300, 0), ("hca", 128, 128, 64, 1300, 32),
+                                                    ("csa", 128, 128, 16, 900, 0), ("hca", 576, 512, 64, 170, 0),
+                                                    ("csa", 576, 512, 64, 500, 0)])
+def test_many_queries_without_keys_in_the_other_forms(ck, empty, kind, d_qk, d_v, H, n, rope):
+    """Padding in calls that the query-pair, split and latent kernels take, with the rule and without."""
+    pos = list(range(600, 600 + n))
+    s = Setup(ck, kind, d_qk, d_v, H, [0] * n, pos, k=64 if kind == "csa" else 0, seed=n, chunk={0: (0, 600, n)})
+    gone = torch.tensor([EMPTY[empty](i, n) for i in range(n)], device="cuda")
+    s.q_pos = torch.where(gone, 1 << 40, s.q_pos)
+    live = (~gone).nonzero().flatten().tolist()
+    for cap, slopes in ((30.0, s.slopes), (0.0, None)):
+        out, lse = s.run(cap, slopes, want=ck.ERR_INVALID_ARG if bool(gone.any()) else 0, rope_dims=rope)
+        assert not bool(out[gone].any()) and bool((lse[gone] == -float("inf")).all())
+        s.check(out, lse, cap, slopes, sorted(set(live[:2] + live[-2:] + live[:: max(1, len(live) // 8)])), rope=rope)
