@@ -33,7 +33,7 @@
 // exponential and half a reciprocal, which two tanh share): 3840 cycles a pair of the
 // first kind; below the cap 10 and 1, 2560 and 2048; without one 3 and 1, 770 and 2048.
 // Measured: ~6,500 a pair, with 15 instructions a logit at half of the issue slots;
-// 4096 queries of 64 heads on 61,440 cached tokens take 163 us.
+// 4096 queries of 64 heads on 61,440 cached tokens take 165 us.
 //
 //   warp 19: describes the items;
 //   warps 20-23: write O / l, a row per thread and a 32-byte sector per store, while
@@ -48,9 +48,9 @@
 // another segment are masked out.
 //
 // Masked keys are multiplied by P = 0, which a NaN or an infinity in a masked key's
-// row would turn into NaN. A row whose output is not finite is therefore taken again
-// by its warp from its own keys only (slow_row), so that no key outside a query's
-// own set can reach its answer.
+// row would turn into NaN. A row whose sum or output is not finite is therefore taken
+// again by its warp from its own keys only (slow_row), so that no key outside a
+// query's own set can reach its answer.
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 #include "score_rule.cuh"
@@ -110,7 +110,8 @@ __device__ __forceinline__ int start32(const AttendParams& p, int t) { return ma
 // not begin with a query) and one segment of them. The rows of its other segments are other items: on their way through
 // the grid the 256 rows come up once per segment they may have (pass), on another CTA each time, so that 16 single tokens
 // with long contexts of their own, which share no key, are 16 CTAs' work (64 such tokens at 1M beside a chunk of 1024, 16
-// heads: 250 us, one CTA for all segments of 256 rows 3,211, the other kernels 341).
+// heads: 250 us, one CTA for all segments of 256 rows 3,211, the other kernels 341). Rows without keys are part of the
+// item of the first segment; 256 rows without any key are none (write_empty).
 struct Segment {
   int s, e;         // queries s .. e - 1 of the item
   int n_w, ntiles;  // window places of the key list, key tiles
@@ -219,8 +220,7 @@ __device__ __forceinline__ uint32_t range_bits(int a, int lo, int hi) {
 }
 
 // 32 bytes per thread: a whole sector in one store where the rows are 32-byte aligned (163 us for 4096 queries on 61,440
-// cached tokens), else two (165 us; callers align their
-// buffers to 16 bytes only)
+// cached tokens; two take 165), else two: callers align their buffers to 16 bytes only
 __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], bool sector) {
   if (sector) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]),
@@ -232,8 +232,8 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&v)[8], b
   }
 }
 
-// The three forms of the kernel. kBounded: a cap of at most kMaxStatic (in log2 units) bounds every logit of a row to
-// ref + cap2 at most, for a reference known beforehand, and the row's own token, or with a negative slope its
+// The three forms of the kernel. kBounded: a cap of at most kMaxStatic (in log2 units) bounds every logit of a row by
+// ref + cap2, for a reference known beforehand, and the row's own token, or with a negative slope its
 // farthest key, is at ref - cap2 at least, so 2^(s - ref) neither overflows fp32 nor vanishes, and the softmax needs no
 // running maximum: no pass for it, no agreement between the halves of a row, no rescaling (181 us -> 176 us
 // when it came). Where that farthest key's page is missing the others may vanish: a sum below kMinSum, which the key
@@ -279,8 +279,8 @@ __device__ __forceinline__ void slow_row(const AttendParams& p, int64_t row, flo
   }
 }
 
-// Pipeline (key tiles numbered g over the CTA's items; stage g % 2):
-//   loader  : look up rows -> wait kempty (P V of tile g - 2) -> TMA gathers -> kfull
+// Pipeline (key tiles numbered g over the CTA's items; stage g % kNS, kNS = 3):
+//   loader  : look up rows -> wait kempty (P V of tile g - 3) -> TMA copies -> kfull
 //   MMA     : S0(0) S1(0), then per key tile (kBounded: per part of it): wait pfull0 -> P V 0(g), S0(g + 1) -> sfull0 (or odone0);
 //             wait pfull1 -> P V 1(g) -> kempty, S1(g + 1) -> sfull1 (or odone1); the last S1 of an item -> qempty
 //   softmax : wait sfull (S here, and every earlier P V of this tile done: O may be rescaled) -> P -> pfull;

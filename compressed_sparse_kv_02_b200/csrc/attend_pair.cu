@@ -29,7 +29,7 @@
 // and the softmax, on eight warps with two threads per head row, applies the rule once and keeps the ruled logits in
 // registers for its exponentials (the plain form reads S twice instead). Its loader warps have 32 rows of a tile each and
 // go their own way: TMA gathers the rows, four per copy, or, where four rows have several sources (ring and pool),
-// cp.async. With one thread per row and cp.async alone 1001 queries of 640 keys took 121 us, with both 98.5; a tile then
+// cp.async. With one thread per row and cp.async alone 1001 queries of 640 keys took 121 us, with both 100; a tile then
 // takes 3,700 cycles, 2,700 of them one softmax pass (a chain of dependent steps: issue slots 39% used, tensor 17%).
 //
 // Shared memory (1024-aligned): Q 32 KB | key stages 4 x 32 KB | P 2 x 16 KB |

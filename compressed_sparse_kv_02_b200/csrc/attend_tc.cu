@@ -48,8 +48,8 @@
 // chain of ~8,400 cycles for bf16 entries and ~16,800 for FP8 (gather 2,700,
 // widening 4,000, S 1,700, softmax 3,700, P V 2,000), with two stages in flight;
 // neither memory nor the tensor cores (16-19% active) set the pace. With a rule,
-// 8 queries up to 1M tokens (HCA, 128 heads) take 37.1 us; 64 FP8 queries of 1152
-// keys (CSA, 128 heads) 98.3 us, 201 before the codes came by TMA, 159 with loader
+// 8 queries up to 1M tokens (HCA, 128 heads) take 36.7 us; 64 FP8 queries of 1152
+// keys (CSA, 128 heads) 99-100 us, 201 before the codes came by TMA, 159 with loader
 // warps that also widened them.
 //
 // RULE is the form with a cap or a distance bias on the logits: the loaders write

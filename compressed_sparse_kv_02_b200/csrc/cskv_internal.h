@@ -87,7 +87,7 @@ cudaError_t launch_append(const FoldParams& p, cudaStream_t st);
 constexpr int kMaxPageSeqs = 4096;  // sequences one call may list
 struct PagePool {
   uint8_t* base;   // null: the layer has no such pool
-  int64_t bytes;   // of one page (a multiple of 16)
+  int64_t bytes;   // of one page (pools: a multiple of 16; a ring of one sequence: of 2)
 };
 struct PageParams {
   int32_t* table;      // [n_seqs, max_pages]
@@ -212,7 +212,7 @@ __device__ __forceinline__ int64_t chunk_row(const AttendParams& p, int seq, int
 cudaError_t launch_attend(AttendParams& p, void* ws, int n_sm, cudaStream_t st);
 bool attend_supported(int d_qk, int d_v, int n_heads, int kv_dtype);
 cudaError_t launch_attend_merge(AttendParams& p, cudaStream_t st);
-// tensor-core (tcgen05) attention for the 576 / 512 latent with heads in groups of 128
+// tensor-core (tcgen05) attention for the 576 / 512 latent with heads in groups of 64
 bool attend_tc_supported(int d_qk, int d_v, int n_heads, int kv_dtype, int n_q, bool rule);
 void attend_tc_plan(AttendParams& p, int n_sm);
 cudaError_t launch_attend_tc(AttendParams& p, int n_sm, cudaStream_t st);

@@ -10,14 +10,14 @@
 // that page choices repeat from call to call. rank_chunk computes it without an
 // inter-CTA wait: each CTA takes kChunk counts and counts the matches in all the
 // chunks before its own by itself. That reads n^2 / (2 kChunk) counts in all, from
-// L2: 8 CTAs and 1 MB at 32,768 pages, 64 CTAs and 33 MB at 262,144.
+// L2: 8 CTAs and 0.5 MB at 32,768 pages, 64 CTAs and 33 MB at 262,144.
 //
 // Bounds: fork, reserve and compaction move bytes (rings and pages, each read and
 // written once, 16 bytes per access, four in flight per thread); free and the
 // table work are a few dependent loads, so latency. Measured: compaction of 12,000
-// pages of the wide latent (1.64 GB) 276 us, 0.91 of the copy rate; 56 branches of
-// 128K tokens forked and their next page reserved (29 MB) 14.6 us; one sequence's
-// fork and reserve 8.7 us, three launches.
+// pages of the wide latent (1.64 GB) 276-280 us, 0.90-0.91 of the copy rate; 56
+// branches of 128K tokens forked and their next page reserved (29 MB) 15.0 us; one
+// sequence's fork and reserve 9.5 us, three launches.
 #include "cskv_device.cuh"
 #include "cskv_internal.h"
 
